@@ -10,6 +10,8 @@
  *   pkv_swap_blocks            block moves between device and page-locked host
  *                              pools (preemption by swapping, 4.3)
  *   pkv_reshape_and_cache      write each new token's K/V into its slot (3.1)
+ *   pkv_qk_norm_rope_and_cache the same with the norm of q and k per head and the
+ *                              rotary embedding in the same pass
  *   pkv_paged_attention_decode single-token attention through the block
  *                              table with the block-wise softmax merge (3.3)
  *   pkv_paged_attention_decode_cascade  decode with shared prompt prefixes
@@ -84,6 +86,7 @@ typedef enum {
 #define PKV_DEVERR_COPY_ID  0x8   /* copy_blocks src/dst outside [0, num_blocks) */
 #define PKV_DEVERR_TIMEOUT  0x10  /* a bounded wait for tensor-core results ran out (pkv_paged_prefill);
                                      the affected rows are not written */
+#define PKV_DEVERR_POSITION 0x20  /* position outside the table of angles (pkv_qk_norm_rope_and_cache) */
 
 /*
  * pkv_reshape_and_cache -- store the K/V of new tokens in their cache slots.
@@ -110,6 +113,53 @@ pkv_status pkv_reshape_and_cache(const void* key, const void* value, pkv_dtype s
                                  int64_t num_blocks, int block_size, int num_kv_heads,
                                  int head_dim, const float* k_scale, const float* v_scale,
                                  pkv_stream_t stream);
+
+/*
+ * pkv_qk_norm_rope_and_cache -- the step before attention in one pass: per-head
+ * RMS norm of q and k, rotary position embedding, and the write of k and v into
+ * their cache slots (in place of two norms, two rotations and
+ * pkv_reshape_and_cache).
+ *
+ * For token i in [0, num_tokens) with s = slot_mapping[i], p = positions[i]:
+ *   s < 0                      : padding; nothing of the token is written;
+ *   s >= num_blocks*block_size : skipped, PKV_DEVERR_SLOT;
+ *   p outside [0, max_position): skipped, PKV_DEVERR_POSITION (rotary_dim > 0);
+ *   else, for every head row x of query[i] and key[i]:
+ *     y = x * (1 / sqrt(mean(x^2) + eps)) * w   (w = q_weight / k_weight, head_dim
+ *         entries of the source dtype; both NULL: y = x and eps is not used);
+ *     for j in [0, rotary_dim/2), c = cos_sin[p][j], d = cos_sin[p][rotary_dim/2 + j]:
+ *       (a, b) -> (a c - b d, b c + a d), where (a, b) = (y[j], y[j + rotary_dim/2]),
+ *       or (y[2j], y[2j+1]) with interleaved != 0; elements from rotary_dim on stay y;
+ *     q rows go to query_out[i], k rows to slot s of key_cache; value[i] goes to slot s
+ *     of value_cache unchanged.
+ * Numerics: fp32 from the loaded values to one rounding at the store; FP8
+ * caches store the E4M3 codes of the quotient by *k_scale / *v_scale as
+ * pkv_reshape_and_cache does (v: the same codes).
+ *
+ * query, key, value: [num_tokens] rows of num_heads / num_kv_heads heads of
+ * head_dim contiguous elements; *_stride elements apart from token to token (at
+ * least the row, a multiple of 16 bytes), so that all three may be column ranges
+ * of one projection output.  query_out: [num_tokens, num_heads, head_dim]
+ * contiguous; may be query itself when query is contiguous, else they must not
+ * overlap.  positions: DEVICE int64 [num_tokens]; cos_sin: DEVICE fp32
+ * [max_position, rotary_dim], both ignored when rotary_dim = 0 (no rotation).
+ * slot_mapping entries >= 0 must be distinct.
+ * dtype f32, f16 or bf16; cache_dtype the same, or FP8_E4M3 with k_scale and
+ * v_scale; head_dim in {64, 128}; rotary_dim a multiple of 16 up to head_dim
+ * (PKV_EUNSUPPORTED otherwise).  All buffers but the scales, slots and positions
+ * 16-byte aligned.
+ */
+pkv_status pkv_qk_norm_rope_and_cache(void* query_out, const void* query, int64_t query_stride,
+                                      const void* key, int64_t key_stride, const void* value,
+                                      int64_t value_stride, pkv_dtype dtype, void* key_cache,
+                                      void* value_cache, pkv_dtype cache_dtype,
+                                      const int64_t* slot_mapping, const int64_t* positions,
+                                      const float* cos_sin, int64_t max_position, int rotary_dim,
+                                      int interleaved, const void* q_weight, const void* k_weight,
+                                      float eps, int64_t num_tokens, int64_t num_blocks,
+                                      int block_size, int num_heads, int num_kv_heads, int head_dim,
+                                      const float* k_scale, const float* v_scale,
+                                      pkv_stream_t stream);
 
 /*
  * pkv_copy_blocks -- copy-on-write duplication of whole physical blocks.

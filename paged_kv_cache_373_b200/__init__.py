@@ -6,7 +6,7 @@ kernels.  There is no CPU fallback; if the library is missing or the tensors
 are not on a CUDA device, the call raises.
 
 Names follow the C entry points without their ``pkv_`` prefix:
-  reshape_and_cache, copy_blocks, swap_blocks, paged_attention_decode, paged_prefill,
+  reshape_and_cache, qk_norm_rope_and_cache, copy_blocks, swap_blocks, paged_attention_decode, paged_prefill,
   paged_attention_decode_noalloc, paged_attention_decode_cascade,
   paged_attention_workspace_bytes, default_num_ctas, decode_step_host, decode_step_layout,
   get_device_error, status_string
@@ -25,11 +25,12 @@ LIB_PATH = os.path.join(_HERE, "libpkv.so")
 PKV_F32, PKV_F16, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2, 3
 PKV_OK, PKV_EINVAL, PKV_EUNSUPPORTED, PKV_ECUDA, PKV_EDEVICE, PKV_ENOBLOCKS = 0, 1, 2, 3, 4, 5
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_SEQ_LEN, DEVERR_COPY_ID, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
+DEVERR_POSITION = 32
 
 _DTYPES = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16,
            torch.uint8: PKV_FP8_E4M3, torch.float8_e4m3fn: PKV_FP8_E4M3}
 
-EXPORTED = ("pkv_reshape_and_cache", "pkv_copy_blocks", "pkv_swap_blocks", "pkv_paged_attention_workspace_bytes",
+EXPORTED = ("pkv_reshape_and_cache", "pkv_qk_norm_rope_and_cache", "pkv_copy_blocks", "pkv_swap_blocks", "pkv_paged_attention_workspace_bytes",
             "pkv_default_num_ctas", "pkv_paged_attention_decode",
             "pkv_paged_attention_decode_noalloc", "pkv_paged_attention_cascade_workspace_bytes",
             "pkv_paged_attention_decode_cascade", "pkv_paged_prefill", "pkv_decode_step_host",
@@ -89,6 +90,10 @@ def lib() -> ctypes.CDLL:
     L.pkv_reshape_and_cache.restype = c_int
     L.pkv_reshape_and_cache.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, i64, i64, c_int, c_int,
                                         c_int, vp, vp, vp]
+    L.pkv_qk_norm_rope_and_cache.restype = c_int
+    L.pkv_qk_norm_rope_and_cache.argtypes = [vp, vp, i64, vp, i64, vp, i64, c_int, vp, vp, c_int, vp, vp, vp,
+                                             i64, c_int, c_int, vp, vp, ctypes.c_float, i64, i64, c_int,
+                                             c_int, c_int, c_int, vp, vp, vp]
     L.pkv_copy_blocks.restype = c_int
     L.pkv_copy_blocks.argtypes = [vp, vp, c_int, vp, i64, i64, ctypes.c_size_t, vp]
     L.pkv_swap_blocks.restype = c_int
@@ -159,6 +164,51 @@ def dtype_code(t: torch.Tensor) -> int:
     return _DTYPES[t.dtype]
 
 
+def _arg(t: Optional[torch.Tensor], name: str, device: torch.device, dtype=None, shape=None) -> Optional[int]:
+    """Address of a contiguous tensor on `device` (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device} (a CUDA device), not {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _scalar(t: Optional[torch.Tensor], name: str, device: torch.device) -> Optional[int]:
+    """Address of a one-element fp32 tensor (an FP8 scale)."""
+    if t is not None and t.numel() != 1:
+        raise ValueError(f"{name} must have one element")
+    return _arg(t, name, device, torch.float32)
+
+
+def _caches(key_cache: torch.Tensor, value_cache: torch.Tensor, device: torch.device):
+    """(addresses, dtype code, shape) of a K/V pool pair [NB, bs, Hkv, D]."""
+    if key_cache.dim() != 4 or value_cache.dtype != key_cache.dtype:
+        raise ValueError("caches must be [num_blocks, block_size, num_kv_heads, head_dim] of one dtype")
+    shape = tuple(key_cache.shape)
+    if key_cache.dtype not in _DTYPES:
+        raise ValueError(f"cache dtype {key_cache.dtype}")
+    return (_arg(key_cache, "key_cache", device), _arg(value_cache, "value_cache", device, shape=shape),
+            _DTYPES[key_cache.dtype], shape)
+
+
+def _launch(fn, device: torch.device, stream, *args) -> None:
+    """Call a library function with `device` current, on `stream` (default: its current one)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, s))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, s))
+
+
 def status_string(status: int) -> str:
     return lib().pkv_status_string(status).decode()
 
@@ -172,6 +222,47 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, k_scale=
         _dev(key), _dev(value), dtype_code(key), _dev(key_cache), _dev(value_cache),
         dtype_code(key_cache), _dev(slot_mapping), T, NB, bs, Hkv, D, _dev(k_scale), _dev(v_scale),
         _stream(stream)))
+
+
+def qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions=None,
+                           cos_sin=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                           interleaved: bool = False, k_scale=None, v_scale=None, stream=None) -> torch.Tensor:
+    """Norm q and k rows per head (where weights are given), rotate them (where cos_sin
+    [max_position, rotary_dim] is given), write q to query_out and k, v to their cache slots.
+    query [T, Hq, D], key/value [T, Hkv, D]: heads contiguous, any token stride
+    (see pkv_qk_norm_rope_and_cache)."""
+    dev, dt = query.device, query.dtype
+    T, Hq, D = query.shape
+    Hkv = key.shape[1]
+    kc, vc, cdt, (NB, bs, chkv, cd) = _caches(key_cache, value_cache, dev)
+    if tuple(key.shape) != (T, Hkv, D) or value.shape != key.shape or (chkv, cd) != (Hkv, D):
+        raise ValueError("query [T, Hq, D], key and value [T, Hkv, D] and the caches disagree")
+    if dt not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"query dtype {dt}")
+    ptrs = []
+    for x, name in ((query, "query"), (key, "key"), (value, "value")):
+        if x.device != dev or x.dtype != dt or not x.is_cuda:
+            raise ValueError(f"{name} must be {dt} on {dev} (a CUDA device)")
+        h = x.shape[1]
+        if (x.stride(2) != 1 and D > 1) or (h > 1 and x.stride(1) != D):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        ptrs += [x.data_ptr(), x.stride(0) if T > 1 else h * D]
+    rot, max_pos, table = 0, 0, None
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_position, rotary_dim]")
+        max_pos, rot = cos_sin.shape
+        table = _arg(cos_sin, "cos_sin", dev, torch.float32)
+        positions = _arg(positions, "positions", dev, torch.int64, (T,))
+    else:
+        positions = None
+    _launch(lib().pkv_qk_norm_rope_and_cache, dev, stream,
+            _arg(query_out, "query_out", dev, dt, (T, Hq, D)), *ptrs, _DTYPES[dt], kc, vc, cdt,
+            _arg(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), positions, table, max_pos, rot,
+            int(bool(interleaved)), _arg(q_weight, "q_weight", dev, dt, (D,)),
+            _arg(k_weight, "k_weight", dev, dt, (D,)), float(eps), T, NB, bs, Hq, Hkv, D,
+            _scalar(k_scale, "k_scale", dev), _scalar(v_scale, "v_scale", dev))
+    return query_out
 
 
 def copy_blocks(key_caches: Sequence[torch.Tensor], value_caches: Sequence[torch.Tensor],
