@@ -14,6 +14,8 @@
  *                              rotary embedding in the same pass
  *   pkv_paged_attention_decode single-token attention through the block
  *                              table with the block-wise softmax merge (3.3)
+ *   pkv_paged_attention_decode_scoremod  the same with capped, biased or windowed scores
+ *   pkv_paged_attention_decode_weights  the same, accumulating each token's attention weight
  *   pkv_paged_attention_decode_cascade  decode with shared prompt prefixes
  *                              read once per group (3.4)
  *   pkv_paged_prefill          chunked-prefill (causal, multi-token) attention
@@ -265,6 +267,64 @@ pkv_status pkv_paged_attention_decode(void* out, const void* query, pkv_dtype q_
                                       float scale, const float* k_scale, const float* v_scale,
                                       void* workspace, size_t workspace_bytes, int num_ctas,
                                       pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_decode_scoremod -- pkv_paged_attention_decode with
+ * modified scores.  For sequence s (L = seq_lens[s], the query at position
+ * p = L - 1) and q head h, over the visible tokens t:
+ *   x = scale * <query[s,h,:], K_t>
+ *   x = softcap * tanh(x / softcap)            if softcap > 0
+ *   x = x - alibi_slopes[h] * (p - t)          if alibi_slopes (DEVICE fp32 [num_heads])
+ *   out[s,h,:] = sum_t softmax(x)_t * V_t      (L == 0 -> zeros)
+ *   t is visible if t < min(prefix_lens[s], L) or p - t < window
+ * prefix_lens: DEVICE int32 [num_seqs] or NULL (no prefix; entries below 0 count
+ * as 0); window = 0: every t < L is visible.  With a window, prefix_lens keeps a
+ * sequence's first tokens attended.
+ * Blocks none of whose tokens are visible are not read and their table entries
+ * not looked at (they may be -1 or stale); within the other blocks, slots that
+ * are not visible have no effect, whatever they hold.
+ * softcap: 0 (none) or positive and finite, 1 / softcap finite; window >= 0
+ * (PKV_EINVAL otherwise).  Slopes must be finite with |slope| * L in fp32 range.
+ * Everything else (types, shapes, workspace, num_ctas, numerics; fp32 scores) as
+ * pkv_paged_attention_decode.
+ */
+pkv_status pkv_paged_attention_decode_scoremod(
+    void* out, const void* query, pkv_dtype q_dtype, const void* key_cache, const void* value_cache,
+    pkv_dtype cache_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int64_t num_blocks, float scale, float softcap, int window,
+    const float* alibi_slopes, const int32_t* prefix_lens, const float* k_scale,
+    const float* v_scale, void* workspace, size_t workspace_bytes, int num_ctas,
+    pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_decode_weights -- pkv_paged_attention_decode that also
+ * accumulates how much each cached token is attended, per kv head (the state
+ * that pkv_evict_tokens selects by).  With a_h the softmax of q head h,
+ *   w[t] = sum of a_h[t] over the g q heads of the kv head,
+ *   weights_out[s, kv, t] = weights_in[s, kv, t] + w[t]    for t < L - 1
+ *   weights_out[s, kv, L-1] = w[L-1]    (the step's own token: its first weight)
+ * and entries t >= L are left as they were.  weights_in, weights_out: DEVICE
+ * fp32 [num_seqs, num_kv_heads, weight_len]; weights_in may be NULL (zeros) or
+ * weights_out itself, else they must not overlap.  A sequence longer than
+ * weight_len sets PKV_DEVERR_SEQ_LEN (its first weight_len entries are written).
+ * The weights are fp32 sums of fp32 probabilities in a fixed order (no atomics);
+ * out is as pkv_paged_attention_decode gives it.
+ * workspace: >= pkv_paged_attention_weights_workspace_bytes(..., max_tokens =
+ * max_blocks_per_seq * block_size, num_ctas) bytes (the split scratch plus one
+ * fp32 score per q head and table slot), 16-byte aligned, no initialisation.
+ * The size function returns 0 for invalid shapes.
+ */
+size_t pkv_paged_attention_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                                   int head_dim, int64_t max_tokens, int num_ctas);
+
+pkv_status pkv_paged_attention_decode_weights(
+    void* out, float* weights_out, const float* weights_in, int64_t weight_len, const void* query,
+    pkv_dtype q_dtype, const void* key_cache, const void* value_cache, pkv_dtype cache_dtype,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+    int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+    const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes,
+    int num_ctas, pkv_stream_t stream);
 
 /*
  * pkv_paged_attention_decode_cascade -- decode attention for batches in which

@@ -8,6 +8,8 @@ are not on a CUDA device, the call raises.
 Names follow the C entry points without their ``pkv_`` prefix:
   reshape_and_cache, qk_norm_rope_and_cache, copy_blocks, swap_blocks, paged_attention_decode, paged_prefill,
   paged_attention_decode_noalloc, paged_attention_decode_cascade,
+  paged_attention_decode_scoremod, paged_attention_decode_weights,
+  paged_attention_weights_workspace_bytes,
   paged_attention_workspace_bytes, default_num_ctas, decode_step_host, decode_step_layout,
   get_device_error, status_string
 """
@@ -32,6 +34,8 @@ _DTYPES = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_B
 
 EXPORTED = ("pkv_reshape_and_cache", "pkv_qk_norm_rope_and_cache", "pkv_copy_blocks", "pkv_swap_blocks", "pkv_paged_attention_workspace_bytes",
             "pkv_default_num_ctas", "pkv_paged_attention_decode",
+            "pkv_paged_attention_decode_scoremod", "pkv_paged_attention_weights_workspace_bytes",
+            "pkv_paged_attention_decode_weights",
             "pkv_paged_attention_decode_noalloc", "pkv_paged_attention_cascade_workspace_bytes",
             "pkv_paged_attention_decode_cascade", "pkv_paged_prefill", "pkv_decode_step_host",
             "pkv_decode_step_layout", "pkv_testing_prefill_timeout",
@@ -106,6 +110,17 @@ def lib() -> ctypes.CDLL:
     L.pkv_paged_attention_decode.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, c_int,
                                              c_int, c_int, c_int, c_int, i64, ctypes.c_float, vp,
                                              vp, vp, ctypes.c_size_t, c_int, vp]
+    L.pkv_paged_attention_decode_scoremod.restype = c_int
+    L.pkv_paged_attention_decode_scoremod.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, c_int,
+                                                      c_int, c_int, c_int, c_int, i64, ctypes.c_float,
+                                                      ctypes.c_float, c_int, vp, vp, vp, vp, vp,
+                                                      ctypes.c_size_t, c_int, vp]
+    L.pkv_paged_attention_weights_workspace_bytes.restype = ctypes.c_size_t
+    L.pkv_paged_attention_weights_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, i64, c_int]
+    L.pkv_paged_attention_decode_weights.restype = c_int
+    L.pkv_paged_attention_decode_weights.argtypes = [vp, vp, vp, i64, vp, c_int, vp, vp, c_int, vp, c_int, vp,
+                                                     c_int, c_int, c_int, c_int, c_int, i64, ctypes.c_float,
+                                                     vp, vp, vp, ctypes.c_size_t, c_int, vp]
     L.pkv_paged_attention_decode_noalloc.restype = c_int
     L.pkv_paged_attention_decode_noalloc.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp,
                                                      c_int, c_int, c_int, c_int, c_int, i64,
@@ -353,6 +368,65 @@ def paged_attention_decode(out, query, key_cache, value_cache, block_tables, seq
         dtype_code(key_cache), _dev(block_tables), block_tables.shape[1], _dev(seq_lens), S, Hq,
         Hkv, D, bs, NB, float(scale), _dev(k_scale), _dev(v_scale), _dev(workspace),
         workspace.numel() * workspace.element_size(), int(num_ctas), _stream(stream)))
+    return out
+
+
+def _decode_args(out, query, key_cache, value_cache, block_tables, seq_lens):
+    """The arguments a decode call shares, checked: (device, shape, leading arguments)."""
+    dev, dt = query.device, query.dtype
+    S, Hq, D = query.shape
+    kc, vc, cdt, (NB, bs, Hkv, cd) = _caches(key_cache, value_cache, dev)
+    if cd != D or dt not in _DTYPES:
+        raise ValueError("query [S, Hq, D] and the caches disagree")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    args = (_arg(query, "query", dev), _DTYPES[dt], kc, vc, cdt,
+            _arg(block_tables, "block_tables", dev, torch.int32), block_tables.shape[1],
+            _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)), S, Hq, Hkv, D, bs, NB)
+    return dev, (S, Hq, Hkv, D, block_tables.shape[1] * bs), _arg(out, "out", dev, dt, (S, Hq, D)), args
+
+
+def paged_attention_decode_scoremod(out, query, key_cache, value_cache, block_tables, seq_lens, scale,
+                                    softcap: float = 0.0, window: int = 0, alibi_slopes=None, prefix_lens=None,
+                                    k_scale=None, v_scale=None, workspace=None, num_ctas: int = 0,
+                                    stream=None) -> torch.Tensor:
+    """Decode attention with modified scores: capped by softcap * tanh(x / softcap), biased by
+    -alibi_slopes[h] * distance (fp32 [Hq]), over the last `window` tokens (0: all) and the first
+    prefix_lens[s] (int32 [S]) (see pkv_paged_attention_decode_scoremod)."""
+    dev, (S, Hq, Hkv, D, _), o, args = _decode_args(out, query, key_cache, value_cache, block_tables, seq_lens)
+    if workspace is None:
+        workspace = alloc_workspace(S, Hq, Hkv, D, num_ctas, device=dev)
+    _launch(lib().pkv_paged_attention_decode_scoremod, dev, stream, o, *args, float(scale), float(softcap),
+            int(window), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
+            _arg(prefix_lens, "prefix_lens", dev, torch.int32, (S,)), _scalar(k_scale, "k_scale", dev),
+            _scalar(v_scale, "v_scale", dev), _arg(workspace, "workspace", dev), workspace.nbytes, int(num_ctas))
+    return out
+
+
+def paged_attention_weights_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                            max_tokens: int, num_ctas: int = 0) -> int:
+    return int(lib().pkv_paged_attention_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                                 max_tokens, num_ctas))
+
+
+def paged_attention_decode_weights(out, weights_out, query, key_cache, value_cache, block_tables, seq_lens, scale,
+                                   weights=None, k_scale=None, v_scale=None, workspace=None, num_ctas: int = 0,
+                                   stream=None) -> torch.Tensor:
+    """Decode attention that adds each cached token's attention weight (summed over the q heads of its
+    kv head) to `weights` (fp32 [S, Hkv, weight_len], None: zeros) and stores it in weights_out, which
+    may be `weights` (see pkv_paged_attention_decode_weights)."""
+    dev, (S, Hq, Hkv, D, cap), o, args = _decode_args(out, query, key_cache, value_cache, block_tables, seq_lens)
+    if weights_out.dim() != 3 or tuple(weights_out.shape[:2]) != (S, Hkv):
+        raise ValueError("weights_out must be [num_seqs, num_kv_heads, weight_len]")
+    wo = _arg(weights_out, "weights_out", dev, torch.float32)
+    wi = _arg(weights, "weights", dev, torch.float32, tuple(weights_out.shape))
+    if workspace is None:
+        with torch.cuda.device(dev):
+            n = paged_attention_weights_workspace_bytes(S, Hq, Hkv, D, cap, num_ctas)
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    _launch(lib().pkv_paged_attention_decode_weights, dev, stream, o, wo, wi, weights_out.shape[2], *args,
+            float(scale), _scalar(k_scale, "k_scale", dev), _scalar(v_scale, "v_scale", dev),
+            _arg(workspace, "workspace", dev), workspace.nbytes, int(num_ctas))
     return out
 
 

@@ -13,14 +13,14 @@
 namespace pkv {
 
 // The decode grid with one of the two length-scan forms.
-template <class C, bool kSuffix, bool kWideScan>
-pkv_status launch_decode_grid(const DecodeLaunchArgs& a, const SuffixArg<kSuffix>& sx, cudaStream_t st) {
+template <class C, class Arg, bool kWideScan>
+pkv_status launch_decode_grid(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_t st) {
     static std::atomic<unsigned long long> configured{0};  // bit per device (< 64)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(PKV_ECUDA, "cudaGetDevice");
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(pkv_decode_kernel<C, kSuffix, kWideScan>,
+        const cudaError_t e = cudaFuncSetAttribute(pkv_decode_kernel<C, Arg, kWideScan>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    C::kSmemBytes);
         if (e != cudaSuccess) return fail(PKV_ECUDA, "smem opt-in: %s", cudaGetErrorString(e));
@@ -28,7 +28,7 @@ pkv_status launch_decode_grid(const DecodeLaunchArgs& a, const SuffixArg<kSuffix
     }
     const DecodeParams& p = *a.params;
     cudaError_t e = cudaSuccess;
-    if constexpr (kSuffix) {
+    if constexpr (Arg::kSuffix) {
         // the cascade suffix pass: a programmatic dependent of the prefix pass
         // (it may start on SMs the prefix pass leaves; see WaitPrimaryAtExit)
         cudaLaunchConfig_t cfg = {};
@@ -41,29 +41,25 @@ pkv_status launch_decode_grid(const DecodeLaunchArgs& a, const SuffixArg<kSuffix
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, pkv_decode_kernel<C, kSuffix, kWideScan>, p, sx);
+        e = cudaLaunchKernelEx(&cfg, pkv_decode_kernel<C, Arg, kWideScan>, p, sx);
     } else {
-        pkv_decode_kernel<C, kSuffix, kWideScan><<<a.grid, C::kWarps * 32, C::kSmemBytes, st>>>(p, sx);
+        pkv_decode_kernel<C, Arg, kWideScan><<<a.grid, C::kWarps * 32, C::kSmemBytes, st>>>(p, sx);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PKV_ECUDA, "decode launch: %s", cudaGetErrorString(e));
     return PKV_OK;
 }
 
-template <class C, bool kSuffix>
-pkv_status launch_decode_k(const DecodeLaunchArgs& a, cudaStream_t st) {
+template <class C, class Arg>
+pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_t st) {
     static_assert(C::kSmemBytes + sizeof(BlockScanSmem) <= 227 * 1024, "shared memory budget");
     const DecodeParams& p = *a.params;
-    SuffixArg<kSuffix> sx{};
-    if constexpr (kSuffix)
-        sx = SuffixArg<true>{a.seq_start, a.part_o, a.part_ml, a.prefix_eff, a.cta_ticket, a.num_groups,
-                             a.prefix_units, a.prefix_tile};
     // the length scans: each warp alone while one round of a warp's scan
     // covers the batch, else once per CTA
-    const pkv_status ds = p.num_seqs > 32 * kScanPerLane ? launch_decode_grid<C, kSuffix, true>(a, sx, st)
-                                                          : launch_decode_grid<C, kSuffix, false>(a, sx, st);
+    const pkv_status ds = p.num_seqs > 32 * kScanPerLane ? launch_decode_grid<C, Arg, true>(a, sx, st)
+                                                          : launch_decode_grid<C, Arg, false>(a, sx, st);
     if (ds != PKV_OK) return ds;
-    if (kSuffix && a.skip_merge) return PKV_OK;  // the cascade's finish pass merges the split units
+    if (Arg::kSuffix && a.skip_merge) return PKV_OK;  // the cascade's finish pass merges the split units
     cudaError_t e = cudaSuccess;
     // the merge kernel is a programmatic dependent launch: its CTAs start
     // while the decode grid drains, locate their unit from the lengths (which
@@ -85,9 +81,9 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (wide)
-        e = cudaLaunchKernelEx(&cfg, pkv_merge_wide_kernel<typename C::q_t, C::D, C::kTT, kSuffix>, p, workers, sx);
+        e = cudaLaunchKernelEx(&cfg, pkv_merge_wide_kernel<typename C::q_t, C::D, C::kTT, Arg>, p, workers, sx);
     else
-        e = cudaLaunchKernelEx(&cfg, pkv_merge_kernel<typename C::q_t, C::D, C::kTT, kSuffix>, p, workers, sx);
+        e = cudaLaunchKernelEx(&cfg, pkv_merge_kernel<typename C::q_t, C::D, C::kTT, Arg>, p, workers, sx);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PKV_ECUDA, "merge launch: %s", cudaGetErrorString(e));
     return PKV_OK;
@@ -96,7 +92,9 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, cudaStream_t st) {
 // Plain decode, or the cascade suffix pass when the call asks for it.
 template <class C>
 pkv_status launch_decode(const DecodeLaunchArgs& a, cudaStream_t st) {
-    return a.suffix ? launch_decode_k<C, true>(a, st) : launch_decode_k<C, false>(a, st);
+    if (!a.suffix) return launch_decode_k<C>(a, SuffixArg<false>{}, st);
+    return launch_decode_k<C>(a, SuffixArg<true>{a.seq_start, a.part_o, a.part_ml, a.prefix_eff, a.cta_ticket,
+                                                 a.num_groups, a.prefix_units, a.prefix_tile}, st);
 }
 
 }  // namespace pkv

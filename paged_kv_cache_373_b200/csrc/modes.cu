@@ -1,0 +1,190 @@
+// modes.cu -- pkv_paged_attention_decode_scoremod and
+// pkv_paged_attention_decode_weights: the decode pass with modified scores, and
+// the decode pass that also accumulates every cached token's attention weight.
+// Both are variants of pkv_decode_kernel (paged_attention.cuh) and share its
+// split of all tiles over the warps of a persistent grid and its exact merge.
+#include <cfloat>
+#include <cmath>
+
+#include "paged_attention.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+pkv_status score_cap(float softcap, float* cap2, float* inv_cap2) {
+    *cap2 = *inv_cap2 = 0.f;
+    if (softcap == 0.f) return PKV_OK;
+    const double c = (double)softcap * 1.4426950408889634;
+    if (!(c > 0.0) || c > (double)FLT_MAX || 1.0 / c > (double)FLT_MAX)
+        return fail(PKV_EINVAL, "softcap must be 0 or positive, finite and not denormal");
+    *cap2 = (float)c;
+    *inv_cap2 = (float)(1.0 / c);
+    return PKV_OK;
+}
+
+namespace {
+
+// ----------------------------------------------------------------------------
+// The last pass of a decode that accumulates attention weights: for every
+// (sequence, kv head) and token t < L
+//   w = sum over the group's q heads of 2^(score - lse),
+//   out[t] = in[t] + w  (t < L - 1),   out[L - 1] = w  (the step's own token).
+// One thread owns a token, so the sum has one order and nothing is atomic.
+// Items of kWeightTokens tokens are dealt to a persistent grid; scores come
+// mostly from L2, where the decode pass has just written them.
+// ----------------------------------------------------------------------------
+constexpr int kWeightThreads = 256, kWeightPer = 4;  // tokens per thread
+constexpr int kWeightTokens = kWeightThreads * kWeightPer;
+
+struct WeightsOut {
+    const float* in;  // [num_seqs, num_kv_heads, len] or null (zeros)
+    float* out;
+    int64_t len;
+};
+
+__global__ void __launch_bounds__(kWeightThreads)
+pkv_weights_kernel(const DecodeParams p, const WeightsArg a, const WeightsOut w) {
+    const WaitPrimaryAtExit<true> wait_at_exit;
+    const int cap = p.max_blocks_per_seq * p.block_size;
+    const int chunks = (cap + kWeightTokens - 1) / kWeightTokens;
+    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads * chunks;
+    bool waited = false;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int64_t u = it / chunks;  // sequence * num_kv_heads + kv head
+        const int s = (int)(u / p.num_kv_heads), kh = (int)(u % p.num_kv_heads);
+        const int t0 = (int)(it % chunks) * kWeightTokens;
+        int L = clamp_len(__ldg(p.seq_lens + s), cap);
+        if (L > w.len) {
+            if (threadIdx.x == 0 && t0 == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
+        }
+        const int n = (int)min((int64_t)L, w.len);
+        if (t0 >= n) continue;
+        if (!waited) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
+        }
+        const int64_t row0 = (int64_t)s * p.num_heads + (int64_t)kh * p.g;
+        float acc[kWeightPer] = {};
+        for (int h = 0; h < p.g; ++h) {
+            const float lse = a.lse[row0 + h];
+            const float* sc = a.scores + (row0 + h) * a.stride + t0 + threadIdx.x;
+            float x[kWeightPer];
+#pragma unroll
+            for (int k = 0; k < kWeightPer; ++k)
+                x[k] = t0 + threadIdx.x + k * kWeightThreads < n ? sc[k * kWeightThreads] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWeightPer; ++k) acc[k] += ex2(x[k] - lse);
+        }
+#pragma unroll
+        for (int k = 0; k < kWeightPer; ++k) {
+            const int t = t0 + threadIdx.x + k * kWeightThreads;
+            if (t >= n) continue;
+            const int64_t at = u * w.len + t;
+            w.out[at] = (w.in && t < L - 1 ? w.in[at] : 0.f) + acc[k];
+        }
+    }
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct WeightsLayout {
+    size_t lse, scores, total;
+};
+bool weights_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int64_t max_tokens, int num_ctas,
+                    WeightsLayout* l) {
+    const size_t dec = decode_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, num_ctas);
+    if (dec == 0 || max_tokens <= 0 || max_tokens > 0x7fffffffLL) return false;
+    const size_t rows = (size_t)num_seqs * num_heads;
+    l->lse = align256(dec);
+    l->scores = l->lse + align256(rows * sizeof(float));
+    l->total = l->scores + rows * (size_t)max_tokens * sizeof(float);
+    return true;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status pkv_paged_attention_decode_scoremod(
+    void* out, const void* query, pkv_dtype q_dtype, const void* key_cache, const void* value_cache,
+    pkv_dtype cache_dtype, const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+    int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+    float softcap, int window, const float* alibi_slopes, const int32_t* prefix_lens, const float* k_scale,
+    const float* v_scale, void* workspace, size_t workspace_bytes, int num_ctas, pkv_stream_t stream) {
+    ModArg m{alibi_slopes, prefix_lens, 0.f, 0.f, window};
+    pkv_status st = score_cap(softcap, &m.cap2, &m.inv_cap2);
+    if (st != PKV_OK) return st;
+    if (window < 0) return fail(PKV_EINVAL, "window < 0");
+    DecodeParams p;
+    DecodeLauncher plain;
+    int grid = 0;
+    st = decode_prepare(&p, &plain, &grid, out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables,
+                        max_blocks_per_seq, seq_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                        num_blocks, scale, k_scale, v_scale, workspace, workspace_bytes, num_ctas);
+    if (st != PKV_OK || num_seqs == 0) return st;
+    DecodeLaunchArgs a{&p, grid};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (cache_dtype) {
+    case PKV_F32: return launch_mod_f32(a, m, head_dim, s);
+    case PKV_F16: return launch_mod_f16(a, m, head_dim, s);
+    case PKV_BF16: return launch_mod_bf16(a, m, head_dim, s);
+    default: return launch_mod_fp8(a, m, q_dtype == PKV_BF16, s);
+    }
+}
+
+extern "C" size_t pkv_paged_attention_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                                              int head_dim, int64_t max_tokens, int num_ctas) {
+    WeightsLayout l;
+    return weights_layout(num_seqs, num_heads, num_kv_heads, head_dim, max_tokens, num_ctas, &l) ? l.total : 0;
+}
+
+extern "C" pkv_status pkv_paged_attention_decode_weights(
+    void* out, float* weights_out, const float* weights_in, int64_t weight_len, const void* query, pkv_dtype q_dtype,
+    const void* key_cache, const void* value_cache, pkv_dtype cache_dtype, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int64_t num_blocks, float scale, const float* k_scale, const float* v_scale, void* workspace,
+    size_t workspace_bytes, int num_ctas, pkv_stream_t stream) {
+    if (weight_len <= 0) return fail(PKV_EINVAL, "weight_len must be positive");
+    if (num_seqs > 0 && !weights_out) return fail(PKV_EINVAL, "null pointer");
+    DecodeParams p;
+    DecodeLauncher plain;
+    int grid = 0;
+    pkv_status st = decode_prepare(&p, &plain, &grid, out, query, q_dtype, key_cache, value_cache, cache_dtype,
+                                   block_tables, max_blocks_per_seq, seq_lens, num_seqs, num_heads, num_kv_heads,
+                                   head_dim, block_size, num_blocks, scale, k_scale, v_scale, workspace,
+                                   workspace_bytes, num_ctas);
+    if (st != PKV_OK || num_seqs == 0) return st;
+    const int64_t max_tokens = (int64_t)max_blocks_per_seq * block_size;
+    WeightsLayout l;
+    if (!weights_layout(num_seqs, num_heads, num_kv_heads, head_dim, max_tokens, num_ctas, &l))
+        return fail(PKV_ECUDA, "cannot size the grid");
+    if (workspace_bytes < l.total)
+        return fail(PKV_EINVAL, "workspace too small: %zu < %zu bytes", workspace_bytes, l.total);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const WeightsArg w{reinterpret_cast<float*>(ws + l.scores), reinterpret_cast<float*>(ws + l.lse), max_tokens};
+    DecodeLaunchArgs a{&p, grid};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (cache_dtype) {
+    case PKV_F32: st = launch_scores_f32(a, w, head_dim, s); break;
+    case PKV_F16: st = launch_scores_f16(a, w, head_dim, s); break;
+    case PKV_BF16: st = launch_scores_bf16(a, w, head_dim, s); break;
+    default: st = launch_scores_fp8(a, w, q_dtype == PKV_BF16, s); break;
+    }
+    if (st != PKV_OK) return st;
+    // the weights pass: a programmatic dependent of the merge pass
+    const int64_t items = (int64_t)num_seqs * num_kv_heads * ((max_tokens + kWeightTokens - 1) / kWeightTokens);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, 8 * (int64_t)pkv_default_num_ctas()));
+    cfg.blockDim = dim3(kWeightThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, pkv_weights_kernel, p, w, WeightsOut{weights_in, weights_out, weight_len});
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "weights launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}

@@ -69,10 +69,12 @@ struct DecodeParams {
 // Cascade suffix pass only (a second kernel argument, empty otherwise): the
 // first token attended per sequence, and for sequences with a non-zero start
 // the unnormalised o and (m, l) partials that replace out.
-template <bool kSuffix> struct SuffixArg {
+template <bool kSuffix_> struct SuffixArg {
+    static constexpr bool kSuffix = false, kMod = false, kWeights = false;
     static constexpr const int32_t* seq_start = nullptr;
 };
 template <> struct SuffixArg<true> {
+    static constexpr bool kSuffix = true, kMod = false, kWeights = false;
     const int32_t* seq_start;  // [num_seqs]
     float* part_o;             // [num_seqs * num_heads * D]
     float2* part_ml;           // [num_seqs * num_heads]
@@ -84,6 +86,31 @@ template <> struct SuffixArg<true> {
     int num_groups;
     int prefix_units;          // prefix units per group (kv heads x row chunks)
     int prefix_tile;           // tokens per prefix tile, 0: the passes run one after the other
+};
+
+// Decode with modified scores (the second kernel argument of that variant):
+//   x = scale q.k;  x = cap tanh(x / cap);  x -= slope_h (p - t),  p = L - 1,
+// over the tokens t < min(prefix, L) and, with a window W, t > p - W.  The
+// kernel works in the log2 domain: x log2(e) = cap2 tanh(x log2(e) / cap2)
+// with cap2 = cap log2(e), and the slopes are scaled as they are loaded.
+struct ModArg {
+    static constexpr bool kSuffix = false, kMod = true, kWeights = false;
+    const float* slopes;         // [num_heads] or null
+    const int32_t* prefix_lens;  // [num_seqs] or null
+    float cap2, inv_cap2;        // 0: no cap
+    int window;                  // 0: no window
+};
+
+// Decode that also accumulates attention weights: every score goes to
+// scores[(s * num_heads + h) * stride + t] (log2 domain) beside the ordinary
+// pass, and the row's log2(sum 2^x) to lse[s * num_heads + h], from which
+// pkv_weights_kernel makes the probabilities.  Storing the scores (4 bytes a
+// head and token, written and read once) costs less than reading K again.
+struct WeightsArg {
+    static constexpr bool kSuffix = false, kMod = false, kWeights = true;
+    float* scores;
+    float* lse;
+    int64_t stride;  // max_blocks_per_seq * block_size
 };
 
 // The cascade's prefix and suffix passes side by side on disjoint SMs: of a
@@ -144,6 +171,49 @@ struct Lens {
     __device__ __forceinline__ int first(int s) const { return first_of(raw_start(s)); }
     __device__ __forceinline__ int eff(int s) const { return eff_of(raw_len(s), raw_start(s)); }
 };
+
+// The ranges of a decode with modified scores, seen as one run of whole
+// tiles: the tiles that hold the prefix, then those from the window's first
+// token on; the `gap` tiles between them are left out, so a sequence's
+// attended length is L - gap * TT.
+struct ModRange {
+    int pre;    // prefix tokens, in [0, L]
+    int first;  // first token of the window: t is attended if t < pre or t >= first
+    int gap;    // tiles left out after the prefix's
+};
+template <int TT>
+struct ModLens {
+    static constexpr bool kHasStart = true;  // "start" entries: the prefix lengths
+    const int32_t* len;
+    const int32_t* pre;  // may be null: no prefix
+    int S, units, cap, window;
+    __device__ __forceinline__ int raw_len(int s) const { return __ldg(len + s); }
+    __device__ __forceinline__ int raw_start(int s) const { return pre ? __ldg(pre + s) : 0; }
+    __device__ __forceinline__ ModRange range(int L, int pr) const {
+        const int Lc = clamp_len(L, cap);
+        const int first = window > 0 && Lc > window ? Lc - window : 0;
+        const int p = clamp_len(pr, Lc);
+        return ModRange{p, first, max(first / TT - (p + TT - 1) / TT, 0)};
+    }
+    __device__ __forceinline__ int eff_of(int L, int pr) const { return clamp_len(L, cap) - range(L, pr).gap * TT; }
+    __device__ __forceinline__ int eff(int s) const { return eff_of(raw_len(s), raw_start(s)); }
+};
+
+template <int TT, bool kSuffix>
+__device__ __forceinline__ Lens<kSuffix> make_lens(const DecodeParams& p, const SuffixArg<kSuffix>& sx) {
+    return Lens<kSuffix>{p.seq_lens, sx.seq_start, p.num_seqs, p.num_kv_heads * p.nch,
+                         p.max_blocks_per_seq * p.block_size};
+}
+template <int TT>
+__device__ __forceinline__ ModLens<TT> make_lens(const DecodeParams& p, const ModArg& m) {
+    return ModLens<TT>{p.seq_lens, m.prefix_lens, p.num_seqs, p.num_kv_heads * p.nch,
+                       p.max_blocks_per_seq * p.block_size, m.window};
+}
+template <int TT>
+__device__ __forceinline__ Lens<false> make_lens(const DecodeParams& p, const WeightsArg&) {
+    return Lens<false>{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads * p.nch, p.max_blocks_per_seq * p.block_size};
+}
+
 template <int TT>
 __device__ __forceinline__ int ntiles_of(int L) { return (L + TT - 1) / TT; }
 
@@ -166,6 +236,16 @@ __device__ __forceinline__ void load_lens(const LN& ln, int s0, int (&v)[E], int
     load_run<E>(ln.len, s0, ln.S, v);
     if constexpr (LN::kHasStart) {
         load_run<E>(ln.start, s0, ln.S, st);
+    } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k) st[k] = 0;
+    }
+}
+template <int E, int TT>
+__device__ __forceinline__ void load_lens(const ModLens<TT>& ln, int s0, int (&v)[E], int (&st)[E]) {
+    load_run<E>(ln.len, s0, ln.S, v);
+    if (ln.pre) {
+        load_run<E>(ln.pre, s0, ln.S, st);
     } else {
 #pragma unroll
         for (int k = 0; k < E; ++k) st[k] = 0;
@@ -396,48 +476,73 @@ __device__ inline SeqHit block_find_seq(const LN& ln, int64_t P, BlockScanSmem& 
 
 // First attended token of the walk's current sequence: a field only when
 // ranges may start past token 0.
-template <bool kStart> struct WalkStart { int st; int nst; };
-template <> struct WalkStart<false> { static constexpr int st = 0; };
+// (WalkOf) and, with modified scores, the range of its tokens.
+template <class LN> struct WalkOf;
+template <> struct WalkOf<Lens<false>> { static constexpr int st = 0; };
+template <> struct WalkOf<Lens<true>> {
+    int st, nst;
+    __device__ __forceinline__ void enter(const Lens<true>& ln, int, int raw) { st = ln.first_of(raw); }
+};
+template <int TT> struct WalkOf<ModLens<TT>> {
+    static constexpr int st = 0;
+    int nst, len;  // len: the sequence's length
+    ModRange mr;
+    __device__ __forceinline__ void enter(const ModLens<TT>& ln, int L, int raw) {
+        len = clamp_len(L, ln.cap);
+        mr = ln.range(L, raw);
+    }
+};
 
 // Walk over a worker's tiles (TT tokens each) in order: (sequence, unit j, tile i).
 // The raw entries of the next sequence are loaded when the walk enters a
 // sequence, so moving on does not wait for a load.
-template <int TT, bool kStart = false>
-struct Walk : WalkStart<kStart> {
+template <int TT, class LN = Lens<false>>
+struct Walk : WalkOf<LN> {
     int s, L, nt, j, i, seg_i0, ord;  // L: attended length
     int nl;                           // raw seq_lens entry of sequence s + 1 (prefetched)
     int64_t T, te;
     bool done;
 
-    __device__ void prefetch_next(const Lens<kStart>& ln) {
+    __device__ void prefetch_next(const LN& ln) {
         const bool in = s + 1 < ln.S;
         nl = in ? ln.raw_len(s + 1) : 0;
-        if constexpr (kStart) this->nst = in ? ln.raw_start(s + 1) : 0;
+        if constexpr (LN::kHasStart) this->nst = in ? ln.raw_start(s + 1) : 0;
     }
-    __device__ void init(const Lens<kStart>& ln, int64_t tb, int64_t te_) {
+    __device__ void init(const LN& ln, int64_t tb, int64_t te_) {
         init(ln, tb, te_, tb < te_ ? find_seq<TT>(ln, tb) : SeqHit{ln.S, 0, 0, 0});
     }
     // h: the sequence holding tile tb (find_seq or block_find_seq)
-    __device__ void init(const Lens<kStart>& ln, int64_t tb, int64_t te_, const SeqHit& h) {
+    __device__ void init(const LN& ln, int64_t tb, int64_t te_, const SeqHit& h) {
         te = te_;
         T = tb;
         done = tb >= te_;
         ord = 0;
         s = 0; L = 0; nt = 1; j = 0; i = 0; seg_i0 = 0; nl = 0;
-        if constexpr (kStart) { this->st = 0; this->nst = 0; }
+        if constexpr (LN::kHasStart) { this->enter(ln, 0, 0); this->nst = 0; }
         if (done) return;
         s = h.s;
         L = ln.eff_of(h.L, h.st);
-        if constexpr (kStart) this->st = ln.first_of(h.st);
+        if constexpr (LN::kHasStart) this->enter(ln, h.L, h.st);
         nt = ntiles_of<TT>(L);
         j = (int)((tb - h.base) / nt);
         i = (int)((tb - h.base) % nt);
         seg_i0 = i;
         prefetch_next(ln);
     }
+    // absolute token of tile i's first row, and the sequence's end
+    __device__ __forceinline__ int token() const {
+        if constexpr (std::is_same<LN, ModLens<TT>>::value)
+            return (i * TT < this->mr.pre ? i : i + this->mr.gap) * TT;
+        else
+            return this->st + i * TT;
+    }
+    __device__ __forceinline__ int end() const {
+        if constexpr (std::is_same<LN, ModLens<TT>>::value) return this->len;
+        else return this->st + L;
+    }
     __device__ bool first() const { return i == seg_i0; }
     __device__ bool last() const { return i == nt - 1 || T == te - 1; }
-    __device__ void advance(const Lens<kStart>& ln) {
+    __device__ void advance(const LN& ln) {
         if (done) return;
         if (++T >= te) { done = true; return; }
         if (++i == nt) {
@@ -450,13 +555,13 @@ struct Walk : WalkStart<kStart> {
                     ++s;
                     if (s < ln.S) {
                         int nst = 0;
-                        if constexpr (kStart) nst = this->nst;
+                        if constexpr (LN::kHasStart) nst = this->nst;
                         L = ln.eff_of(nl, nst);
-                        if constexpr (kStart) this->st = ln.first_of(nst);
+                        if constexpr (LN::kHasStart) this->enter(ln, nl, nst);
                         prefetch_next(ln);
                     } else {
                         L = TT;
-                        if constexpr (kStart) this->st = 0;
+                        if constexpr (LN::kHasStart) this->enter(ln, 0, 0);
                     }
                     nt = ntiles_of<TT>(L);
                 } while (nt == 0);
@@ -545,12 +650,12 @@ struct Sink {
     int nh;
 };
 
-// kPart: the cascade suffix pass, whose whole units may be partials.
-template <typename QT, bool kPart>
-__device__ __forceinline__ void sink_write(const DecodeParams& p, const SuffixArg<kPart>& sx, const Sink& k,
+// (The whole units of the cascade suffix pass may be partials.)
+template <typename QT, class Arg>
+__device__ __forceinline__ void sink_write(const DecodeParams& p, const Arg& sx, const Sink& k,
                                            int D, int h, int d, float o, float l, float vscale) {
     if (h >= k.nh) return;
-    if constexpr (kPart) {
+    if constexpr (Arg::kSuffix) {
         if (k.part) {
             sx.part_o[(k.row0 + h) * D + d] = o * vscale;
             return;
@@ -561,6 +666,64 @@ __device__ __forceinline__ void sink_write(const DecodeParams& p, const SuffixAr
         *out = from_f32<QT>(l > 0.f ? o * vscale / l : 0.f);
     } else {
         p.ws_o[(k.seg * p.hpu + h) * D + d] = o * vscale;
+    }
+}
+
+// What a tile's math needs to know of its place, beyond the number of rows
+// inside the sequence: nothing for the plain variants.
+template <class Arg> struct TileInfo {};
+template <> struct TileInfo<ModArg> {
+    const float* slopes;  // of the unit's first head, or null
+    int tok;              // absolute token of the tile's first row
+    int pos;              // the query's position (length - 1)
+    int pre, first;       // visible: t < pre or t >= first
+    bool edge;            // some row inside the sequence is not visible
+    __device__ __forceinline__ bool hidden(int row) const {
+        const int t = tok + row;
+        return edge && t >= pre && t < first;
+    }
+};
+template <> struct TileInfo<WeightsArg> {
+    float* row;      // scores of the unit's first head at the tile's first token
+    int64_t stride;  // floats between heads
+    int nh;
+};
+
+// tanh y, |relative error| < 2^-22: below 1/2 an odd polynomial (a minimax fit
+// of (tanh y) / y - 1 in y^2, off by 1.5e-8 at most), above it
+// 1 - 2 / (1 + e^2|y|) with the hardware's 2^x and reciprocal, whose sum is at
+// least 0.46 there and loses no digits to the subtraction.  y = +-inf gives +-1.
+__device__ __forceinline__ float tanh_poly(float y) {
+    const float z = y * y;
+    float q = fmaf(z, 0.01724149100482464f, -0.05304549261927605f);
+    q = fmaf(z, q, 0.13325878977775574f);
+    q = fmaf(z, q, -0.333331435918808f);
+    return fmaf(y * z, q, y);
+}
+__device__ __forceinline__ float tanh_exp(float y) {
+    const float e = ex2(fabsf(y) * 2.885390081777927f);  // e^(2|y|)
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return copysignf(fmaf(-2.f, r, 1.f), y);
+}
+
+// N scores (log2 domain) capped in place.  Both forms are a select away from
+// each other, so the choice is made per lane for all its scores: the exponential
+// form costs two more of the special-function unit's operations per score.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&x)[N], const ModArg& m) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] *= m.inv_cap2;
+        big = fmaxf(big, fabsf(x[i]));
+    }
+    if (big < 0.5f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = m.cap2 * tanh_poly(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = m.cap2 * (fabsf(x[i]) < 0.5f ? tanh_poly(x[i]) : tanh_exp(x[i]));
     }
 }
 
@@ -652,15 +815,23 @@ struct MmaConsumer {
         }
     }
 
+    float sb0, sb1;      // modified scores: the slopes of heads 2 tig, 2 tig + 1 (log2 domain)
+    __device__ void load_slopes(const float* slopes, int nh) {
+        const int tig = threadIdx.x & 3;
+        sb0 = 2 * tig < nh ? __ldg(slopes + 2 * tig) * 1.4426950408889634f : 0.f;
+        sb1 = 2 * tig + 1 < nh ? __ldg(slopes + 2 * tig + 1) * 1.4426950408889634f : 0.f;
+    }
+
     // One tile of TT = 16 * NM tokens: S^T per 16-token m-tile, one online
     // softmax step over the whole tile, then P.V with one k-step per m-tile.
-    __device__ void tile(uint8_t* kt, uint8_t* vt, int valid) {
+    template <class Arg>
+    __device__ void tile(uint8_t* kt, uint8_t* vt, int valid, const Arg& ax, const TileInfo<Arg>& ti) {
         constexpr int TT = C::kTT, NM = TT / 16;
         const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
         // rows >= valid: zero-filled by issue_tile for 16-bit caches; FP8
         // codes are loaded as stored and zeroed here, so that unused slots
         // (never written, any bits) cannot reach the P.V product
-        if constexpr (C::kPath == Path::kFp8)
+        if constexpr (C::kPath == Path::kFp8 && !Arg::kMod)
             if (valid < TT) zero_tail_rows<C::kNSub, TT>(vt, valid, lane);
         const uint32_t kb = smem_u32(kt), vb = smem_u32(vt);
         float x[NM][4];
@@ -699,6 +870,29 @@ struct MmaConsumer {
             // scores S^T[token][head]: (gid, 2tig), (gid, 2tig+1), (gid+8, 2tig), (gid+8, 2tig+1)
             x[m][0] = (sa[0] + sb[0]) * sl0; x[m][1] = (sa[1] + sb[1]) * sl1;
             x[m][2] = (sa[2] + sb[2]) * sl0; x[m][3] = (sa[3] + sb[3]) * sl1;
+            if constexpr (Arg::kMod) {
+                if (ax.cap2 > 0.f) cap_scores(x[m], ax);
+                if (ti.slopes) {
+                    const float d0 = (float)(ti.pos - (ti.tok + 16 * m + gid)), d1 = d0 - 8.f;
+                    x[m][0] = fmaf(-sb0, d0, x[m][0]); x[m][1] = fmaf(-sb1, d0, x[m][1]);
+                    x[m][2] = fmaf(-sb0, d1, x[m][2]); x[m][3] = fmaf(-sb1, d1, x[m][3]);
+                }
+                if (ti.hidden(16 * m + gid)) x[m][0] = x[m][1] = -INFINITY;
+                if (ti.hidden(16 * m + gid + 8)) x[m][2] = x[m][3] = -INFINITY;
+            }
+            if constexpr (Arg::kWeights) {
+                // 8 lanes of a head hold 8 neighbouring tokens: whole 32-byte sectors
+                float* w0 = ti.row + (int64_t)(2 * tig) * ti.stride + 16 * m + gid;
+                const bool r0 = 16 * m + gid < valid, r1 = 16 * m + gid + 8 < valid;
+                if (2 * tig < ti.nh) {
+                    if (r0) w0[0] = x[m][0];
+                    if (r1) w0[8] = x[m][2];
+                }
+                if (2 * tig + 1 < ti.nh) {
+                    if (r0) w0[ti.stride] = x[m][1];
+                    if (r1) w0[ti.stride + 8] = x[m][3];
+                }
+            }
             if (16 * m + gid >= valid) x[m][0] = x[m][1] = -INFINITY;
             if (16 * m + gid + 8 >= valid) x[m][2] = x[m][3] = -INFINITY;
         }
@@ -751,9 +945,15 @@ struct MmaConsumer {
                 ls0 += e0 + e2;
                 ls1 += e1 + e3;
             } else {
+                if constexpr (Arg::kWeights) {  // the weights' normaliser: P before its rounding
+                    ls0 += e0 + e2;
+                    ls1 += e1 + e3;
+                }
                 const float2 p0 = unpack2<false>(X0), p1 = unpack2<false>(X1);
-                ls0 += p0.x + p1.x;  // normaliser from the rounded P actually used
-                ls1 += p0.y + p1.y;
+                if constexpr (!Arg::kWeights) {
+                    ls0 += p0.x + p1.x;  // normaliser from the rounded P actually used
+                    ls1 += p0.y + p1.y;
+                }
                 c0[m] = c1[m] = 0u;
             }
             b0[m] = movm_trans(X0);  // P^T as mma B
@@ -802,8 +1002,9 @@ struct MmaConsumer {
     }
 
     // End of a unit segment: the output (whole unit) or a partial (split).
-    template <bool kPart>
-    __device__ void finish(const DecodeParams& p, const SuffixArg<kPart>& sx, const Sink& k, float vscale) {
+    template <class Arg>
+    __device__ void finish(const DecodeParams& p, const Arg& sx, const Sink& k, float vscale) {
+        constexpr bool kPart = Arg::kSuffix;
         using QT = typename C::q_t;
         const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
         float a0 = l0, a1 = l1;
@@ -813,6 +1014,12 @@ struct MmaConsumer {
             a1 += __shfl_xor_sync(kFull, a1, o);
         }
         const int h0 = 2 * tig, h1 = 2 * tig + 1;
+        if constexpr (Arg::kWeights) {
+            if (!k.split && gid == 0) {
+                if (h0 < k.nh) sx.lse[k.row0 + h0] = m0 + log2f(a0);
+                if (h1 < k.nh) sx.lse[k.row0 + h1] = m1 + log2f(a1);
+            }
+        }
         bool to_out = !k.split;
         if constexpr (kPart) to_out = to_out && !k.part;
         if (to_out) {
@@ -852,10 +1059,10 @@ struct MmaConsumer {
             int d0, d1;
             if constexpr (!kFp8) { d0 = 16 * mi + gid; d1 = d0 + 8; }
             else { d0 = 16 * gid + 2 * mi; d1 = d0 + 1; }
-            sink_write<QT, kPart>(p, sx, k, D, h0, d0, acc[mi][0], a0, vscale);
-            sink_write<QT, kPart>(p, sx, k, D, h1, d0, acc[mi][1], a1, vscale);
-            sink_write<QT, kPart>(p, sx, k, D, h0, d1, acc[mi][2], a0, vscale);
-            sink_write<QT, kPart>(p, sx, k, D, h1, d1, acc[mi][3], a1, vscale);
+            sink_write<QT, Arg>(p, sx, k, D, h0, d0, acc[mi][0], a0, vscale);
+            sink_write<QT, Arg>(p, sx, k, D, h1, d0, acc[mi][1], a1, vscale);
+            sink_write<QT, Arg>(p, sx, k, D, h0, d1, acc[mi][2], a0, vscale);
+            sink_write<QT, Arg>(p, sx, k, D, h1, d1, acc[mi][3], a1, vscale);
         }
         if constexpr (kPart) {
             if (gid == 0 && (k.split || k.part)) {
@@ -901,7 +1108,9 @@ struct F32Consumer {
         for (int h = 0; h < kHeadsPerUnit; ++h)
             qv[h] = (h < nh) ? q4[h * CPR + c] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __device__ void tile(uint8_t* kt, uint8_t* vt, int valid) {
+    __device__ void load_slopes(const float*, int) {}
+    template <class Arg>
+    __device__ void tile(uint8_t* kt, uint8_t* vt, int valid, const Arg& ax, const TileInfo<Arg>& ti) {
         const int lane = threadIdx.x & 31, c = lane % CPR, rh = lane / CPR;
         float4 kr[NIT];
 #pragma unroll
@@ -938,6 +1147,19 @@ struct F32Consumer {
                 }
             }
             float x = (tok < valid) ? v[0] * sl : -INFINITY;
+            if constexpr (Arg::kMod) {
+                if (ax.cap2 > 0.f && tok < valid) {
+                    float y[1] = {x};
+                    cap_scores(y, ax);
+                    x = y[0];
+                }
+                if (ti.slopes)
+                    x = fmaf(-__ldg(ti.slopes + h) * 1.4426950408889634f, (float)(ti.pos - (ti.tok + tok)), x);
+                if (ti.hidden(tok)) x = -INFINITY;
+            }
+            if constexpr (Arg::kWeights) {  // two lanes hold each token's score
+                if (!(lane & 1) && tok < valid) ti.row[h * ti.stride + tok] = x;
+            }
             float mx = x;
 #pragma unroll
             for (int o = 2; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
@@ -962,8 +1184,9 @@ struct F32Consumer {
             }
         }
     }
-    template <bool kPart>
-    __device__ void finish(const DecodeParams& p, const SuffixArg<kPart>& sx, const Sink& k, float vscale) {
+    template <class Arg>
+    __device__ void finish(const DecodeParams& p, const Arg& sx, const Sink& k, float vscale) {
+        constexpr bool kPart = Arg::kSuffix;
         const int lane = threadIdx.x & 31, c = lane % CPR, rh = lane / CPR;
 #pragma unroll
         for (int h = 0; h < kHeadsPerUnit; ++h) {
@@ -975,11 +1198,14 @@ struct F32Consumer {
                 a.x += __shfl_xor_sync(kFull, a.x, 16); a.y += __shfl_xor_sync(kFull, a.y, 16);
                 a.z += __shfl_xor_sync(kFull, a.z, 16); a.w += __shfl_xor_sync(kFull, a.w, 16);
             }
+            if constexpr (Arg::kWeights) {
+                if (!k.split && lane == 0 && h < k.nh) sx.lse[k.row0 + h] = m[h] + log2f(ls);
+            }
             if (rh == 0) {
-                sink_write<float, kPart>(p, sx, k, D, h, 4 * c + 0, a.x, ls, vscale);
-                sink_write<float, kPart>(p, sx, k, D, h, 4 * c + 1, a.y, ls, vscale);
-                sink_write<float, kPart>(p, sx, k, D, h, 4 * c + 2, a.z, ls, vscale);
-                sink_write<float, kPart>(p, sx, k, D, h, 4 * c + 3, a.w, ls, vscale);
+                sink_write<float, Arg>(p, sx, k, D, h, 4 * c + 0, a.x, ls, vscale);
+                sink_write<float, Arg>(p, sx, k, D, h, 4 * c + 1, a.y, ls, vscale);
+                sink_write<float, Arg>(p, sx, k, D, h, 4 * c + 2, a.z, ls, vscale);
+                sink_write<float, Arg>(p, sx, k, D, h, 4 * c + 3, a.w, ls, vscale);
             }
             if constexpr (kPart) {
                 if (lane == 0 && h < k.nh) {
@@ -1065,15 +1291,16 @@ struct IssueLane {
 // Issue the async loads of the walk's current tile (and, on a unit's first
 // tile, of its q rows) into stage `stg` / q slot `qslot`.  lg_bs: log2 of
 // the block size (16 or 32 tokens).
-template <class C, bool kStart>
-__device__ __forceinline__ void issue_tile(const DecodeParams& p, const Walk<C::kTT, kStart>& w, TablePrefetch& tp,
+template <class C, class LN>
+__device__ __forceinline__ void issue_tile(const DecodeParams& p, const Walk<C::kTT, LN>& w, TablePrefetch& tp,
                                            const IssueLane<C>& il, int lg_bs, uint8_t* stg, uint8_t* qslot) {
     const int lane = threadIdx.x & 31;
     const int2 hc = unit_head(w.j, p.nch);
     const int kh = hc.x, c = hc.y;
-    const int tok = w.st + w.i * C::kTT;  // absolute token of the tile's first row (a multiple of 16)
+    constexpr bool kMod = std::is_same<LN, ModLens<C::kTT>>::value;
+    const int tok = w.token();  // absolute token of the tile's first row (a multiple of 16)
     const int bmask = (1 << lg_bs) - 1;
-    const int nblk = (w.st + w.L + bmask) >> lg_bs;
+    const int nblk = (w.end() + bmask) >> lg_bs;
     const int b0 = tok >> lg_bs;
     auto checked = [&](int ph) {
         if (ph < 0 || ph >= p.num_blocks) {
@@ -1102,8 +1329,18 @@ __device__ __forceinline__ void issue_tile(const DecodeParams& p, const Walk<C::
     // rows of the tile inside the sequence (16-bit caches zero-fill the rest:
     // measured faster there; the FP8 and fp32 tiles mask or zero them after
     // the load, which keeps their kernels' code and registers smaller)
-    const int nvalid = C::kPath == Path::kMma16 ? w.L - w.i * C::kTT : C::kTT;
-    if (nvalid >= C::kTT) {
+    const int nvalid = C::kPath == Path::kMma16 || kMod ? w.L - w.i * C::kTT : C::kTT;
+    // modified scores: rows inside the sequence that the query does not attend
+    // (the tiles at the window's first and the prefix's last token) are
+    // zero-filled as well, whatever their slots hold
+    bool whole = nvalid >= C::kTT;
+    int hid0 = 0, hid1 = 0;  // hidden rows [hid0, hid1)
+    if constexpr (kMod) {
+        hid0 = max(w.mr.pre - tok, 0);
+        hid1 = w.mr.first - tok;
+        whole = whole && hid0 >= min(hid1, C::kTT);
+    }
+    if (whole) {
 #pragma unroll
         for (int it = 0; it < C::kTT / C::kRowsPerInst; ++it) {
             // rows >= 16 exactly when it * kRowsPerInst >= 16
@@ -1120,7 +1357,9 @@ __device__ __forceinline__ void issue_tile(const DecodeParams& p, const Walk<C::
         for (int it = 0; it < C::kTT / C::kRowsPerInst; ++it) {
             const int64_t off = (it * C::kRowsPerInst >= 16 ? base1 : base0) + it * il.gstep;
             const uint32_t so = il.so[it % IssueLane<C>::kP] + (it / IssueLane<C>::kP) * 1024;
-            const uint32_t n = it * C::kRowsPerInst + il.r0 < nvalid ? 16u : 0u;
+            const int row = it * C::kRowsPerInst + il.r0;
+            uint32_t n = row < nvalid ? 16u : 0u;
+            if constexpr (kMod) n = row >= hid0 && row < hid1 ? 0u : n;
             cp_async16_zfill(kdst + so, kl + off, n);
             cp_async16_zfill(vdst + so, vl + off, n);
         }
@@ -1143,10 +1382,10 @@ __device__ __forceinline__ void issue_tile(const DecodeParams& p, const Walk<C::
 // whose results it does not read: it may run beside the prefix pass's last
 // CTAs, but it completes only after that grid, so that the passes after it
 // see every prefix partial.  Every exit of a suffix CTA waits.
-template <bool kSuffix>
+template <bool kWait>
 struct WaitPrimaryAtExit {
     __device__ ~WaitPrimaryAtExit() {
-        if constexpr (kSuffix) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if constexpr (kWait) asm volatile("griddepcontrol.wait;" ::: "memory");
     }
 };
 
@@ -1154,9 +1393,11 @@ struct WaitPrimaryAtExit {
 // scan does not cover); false: each warp scans alone, with no CTA barrier.
 // Two instantiations rather than a branch: with the CTA-wide form compiled
 // in, a cold-started tiny batch measured 4 us slower.
-template <class C, bool kSuffix, bool kWideScan>
+// Arg: the variant's own argument (SuffixArg, ModArg, WeightsArg).
+template <class C, class Arg, bool kWideScan>
 __global__ void __launch_bounds__(C::kWarps * 32, 1)
-pkv_decode_kernel(const DecodeParams p, const SuffixArg<kSuffix> sx) {
+pkv_decode_kernel(const DecodeParams p, const Arg sx) {
+    constexpr bool kSuffix = Arg::kSuffix;
     const WaitPrimaryAtExit<kSuffix> wait_at_exit;
     // let the merge grid (a programmatic dependent launch) be scheduled now:
     // its CTAs locate their units while this grid runs and wait for its
@@ -1169,8 +1410,8 @@ pkv_decode_kernel(const DecodeParams p, const SuffixArg<kSuffix> sx) {
     uint8_t* stages = smem + warp * C::kWarpBytes;
     uint8_t* qslots = stages + C::kStages * C::kStageBytes;
 
-    const Lens<kSuffix> ln{p.seq_lens, sx.seq_start, p.num_seqs, p.num_kv_heads * p.nch,
-                           p.max_blocks_per_seq * p.block_size};
+    const auto ln = make_lens<C::kTT>(p, sx);
+    using LN = std::remove_const_t<decltype(ln)>;
     int64_t workers = (int64_t)gridDim.x * C::kWarps;
     int64_t cta = blockIdx.x;
     if constexpr (kSuffix) {
@@ -1199,7 +1440,7 @@ pkv_decode_kernel(const DecodeParams p, const SuffixArg<kSuffix> sx) {
     // the total and every warp's first tile
     bool bad_len = false;
     int64_t W, tb, te;
-    Walk<C::kTT, kSuffix> iw, cw;  // issue walk (runs kStages-1 tiles ahead) and compute walk
+    Walk<C::kTT, LN> iw, cw;  // issue walk (runs kStages-1 tiles ahead) and compute walk
     if constexpr (!kWideScan) {
         W = total_tiles<C::kTT>(ln, &bad_len);
         side_by_side(W);
@@ -1251,17 +1492,30 @@ pkv_decode_kernel(const DecodeParams p, const SuffixArg<kSuffix> sx) {
         if (cw.first()) {
             cs.load_q(qslots + (cw.ord % C::kStages) * C::kQSlot, nh, p.scale_log2, kscale);
             cs.reset();
+            if constexpr (Arg::kMod)
+                if (sx.slopes) cs.load_slopes(sx.slopes + kh * p.g + kHeadsPerUnit * c, nh);
+        }
+        TileInfo<Arg> ti;
+        if constexpr (Arg::kMod) {
+            const int tok = cw.token();
+            const bool edge = tok < cw.mr.first && tok + C::kTT > cw.mr.pre;
+            ti = TileInfo<Arg>{sx.slopes ? sx.slopes + kh * p.g + kHeadsPerUnit * c : nullptr, tok, cw.len - 1,
+                               cw.mr.pre, cw.mr.first, edge};
+        } else if constexpr (Arg::kWeights) {
+            const int64_t row0 = (int64_t)cw.s * p.num_heads + (int64_t)kh * p.g + kHeadsPerUnit * c;
+            ti = TileInfo<Arg>{sx.scores + row0 * sx.stride + cw.token(), sx.stride, nh};
         }
         uint8_t* kt = stages + (n % C::kStages) * C::kStageBytes;
-        cs.tile(kt, kt + C::kTensorTile, min(C::kTT, cw.L - cw.i * C::kTT));
+        cs.tile(kt, kt + C::kTensorTile, min(C::kTT, cw.L - cw.i * C::kTT), sx, ti);
         if (cw.last()) {
             Sink k;
             k.split = (cw.seg_i0 != 0) || (cw.i != cw.nt - 1);
-            k.part = kSuffix && !k.split && cw.st > 0;
+            k.part = false;
+            if constexpr (kSuffix) k.part = !k.split && cw.st > 0;
             k.seg = wid + ((int64_t)cw.s * p.num_kv_heads + kh) * p.nch + c;
             k.row0 = (int64_t)cw.s * p.num_heads + (int64_t)kh * p.g + kHeadsPerUnit * c;
             k.nh = nh;
-            cs.template finish<kSuffix>(p, sx, k, vscale);
+            cs.finish(p, sx, k, vscale);
         }
         __syncwarp();  // every lane is done with this stage before it is refilled
         cw.advance(ln);
@@ -1277,16 +1531,18 @@ pkv_decode_kernel(const DecodeParams p, const SuffixArg<kSuffix> sx) {
 // row; CTA 0 zeroes the empty sequences.  Partials are folded in worker order, four segments
 // per step (their loads in flight together, M updated once per step).
 // ----------------------------------------------------------------------------
-template <typename QT, int D, int TT, bool kSuffix>
+template <typename QT, int D, int TT, class Arg>
 __global__ void __launch_bounds__(256)
-pkv_merge_kernel(const DecodeParams p, int64_t workers, const SuffixArg<kSuffix> sx) {
+pkv_merge_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
+    constexpr bool kSuffix = Arg::kSuffix;
+    // the weights pass reads what the decode grid wrote: this grid may not end before it
+    const WaitPrimaryAtExit<Arg::kWeights> wait_at_exit;
     // a following programmatic dependent (the cascade's combine pass) may be
     // scheduled now; it waits for this grid before reading
-    if constexpr (kSuffix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (kSuffix || Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t b = blockIdx.x;
-    const Lens<kSuffix> ln{p.seq_lens, sx.seq_start, p.num_seqs, p.num_kv_heads * p.nch,
-                           p.max_blocks_per_seq * p.block_size};
+    const auto ln = make_lens<TT>(p, sx);
     if (b == 0) {
         // sequences with nothing to attend: zero output (or an empty partial
         // (m, l) = (-inf, 0) for a cascade suffix); warps scan 32 at a time
@@ -1379,6 +1635,8 @@ pkv_merge_kernel(const DecodeParams p, int64_t workers, const SuffixArg<kSuffix>
             return;
         }
     }
+    if constexpr (Arg::kWeights)
+        if (lane == 0) sx.lse[row0 + h] = M + log2f(ls);
     QT* out = reinterpret_cast<QT*>(p.out) + (row0 + h) * D;
 #pragma unroll
     for (int e = 0; e < PER; ++e) out[lane + 32 * e] = from_f32<QT>(ls > 0.f ? o[e] / ls : 0.f);
@@ -1402,16 +1660,17 @@ struct MergeTask {
     int s;           // its sequence
 };
 
-template <typename QT, int D, int TT, bool kSuffix>
+template <typename QT, int D, int TT, class Arg>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const SuffixArg<kSuffix> sx) {
+pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
+    constexpr bool kSuffix = Arg::kSuffix;
+    const WaitPrimaryAtExit<Arg::kWeights> wait_at_exit;
     // a following programmatic dependent (the cascade's combine pass) may be
     // scheduled now; it waits for this grid before reading
-    if constexpr (kSuffix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (kSuffix || Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t gw = (int64_t)blockIdx.x * kMergeWarps + warp;
-    const Lens<kSuffix> ln{p.seq_lens, sx.seq_start, p.num_seqs, p.num_kv_heads * p.nch,
-                           p.max_blocks_per_seq * p.block_size};
+    const auto ln = make_lens<TT>(p, sx);
     // sequences with nothing to attend (independent of the decode grid): zero
     // output, or an empty partial (m, l) = (-inf, 0) for a cascade suffix; a
     // warp per 32 sequences
@@ -1518,6 +1777,8 @@ pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const SuffixArg<kSu
                 continue;
             }
         }
+        if constexpr (Arg::kWeights)
+            if (lane == 0) sx.lse[t.row0 + h] = M + log2f(ls);
         QT* out = reinterpret_cast<QT*>(p.out) + (t.row0 + h) * D;
 #pragma unroll
         for (int e = 0; e < PER; ++e) out[lane + 32 * e] = from_f32<QT>(ls > 0.f ? o[e] / ls : 0.f);

@@ -71,4 +71,22 @@ pkv_status launch_decode_bf16_d128(const DecodeLaunchArgs&, cudaStream_t);
 pkv_status launch_decode_fp8_qf16_d128(const DecodeLaunchArgs&, cudaStream_t);
 pkv_status launch_decode_fp8_qbf16_d128(const DecodeLaunchArgs&, cudaStream_t);
 
+
+// Decode with modified scores, and with the scores kept (modes_*.cu): the
+// decode and merge passes.  Chosen by dtype in modes.cu after decode_prepare.
+struct ModArg;
+struct WeightsArg;
+pkv_status launch_mod_f32(const DecodeLaunchArgs&, const ModArg&, int head_dim, cudaStream_t);
+pkv_status launch_mod_f16(const DecodeLaunchArgs&, const ModArg&, int head_dim, cudaStream_t);
+pkv_status launch_mod_bf16(const DecodeLaunchArgs&, const ModArg&, int head_dim, cudaStream_t);
+pkv_status launch_mod_fp8(const DecodeLaunchArgs&, const ModArg&, bool q_bf16, cudaStream_t);
+pkv_status launch_scores_f32(const DecodeLaunchArgs&, const WeightsArg&, int head_dim, cudaStream_t);
+pkv_status launch_scores_f16(const DecodeLaunchArgs&, const WeightsArg&, int head_dim, cudaStream_t);
+pkv_status launch_scores_bf16(const DecodeLaunchArgs&, const WeightsArg&, int head_dim, cudaStream_t);
+pkv_status launch_scores_fp8(const DecodeLaunchArgs&, const WeightsArg&, bool q_bf16, cudaStream_t);
+
+// The cap of modified scores in the log2 domain (cap2 = 0: none); PKV_EINVAL
+// for a cap that is negative, not finite or too small for fp32 arithmetic.
+pkv_status score_cap(float softcap, float* cap2, float* inv_cap2);
+
 }  // namespace pkv
