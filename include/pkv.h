@@ -20,6 +20,7 @@
  *                              read once per group (3.4)
  *   pkv_paged_prefill          chunked-prefill (causal, multi-token) attention
  *                              through the block table
+ *   pkv_paged_prefill_scoremod the same with capped, biased or windowed scores
  * and, in pkv_block_manager.h, the host block manager that produces the
  * tables, slots and copy-on-write pairs.
  *
@@ -406,6 +407,28 @@ pkv_status pkv_paged_prefill(void* out, const void* query, pkv_dtype q_dtype, co
                              const int32_t* seq_lens, const int32_t* query_start, int num_seqs,
                              int64_t num_query_tokens, int num_heads, int num_kv_heads, int head_dim,
                              int block_size, int64_t num_blocks, float scale, pkv_stream_t stream);
+
+/*
+ * pkv_paged_prefill_scoremod -- pkv_paged_prefill with modified scores: the chunk
+ * form of pkv_paged_attention_decode_scoremod.  A row at position p of sequence s
+ * (L = seq_lens[s]) attends the tokens
+ *   t < min(prefix_lens[s], L), whatever p is (a prefix that sees all of itself), or
+ *   t <= p with p - t < window (window = 0: every t <= p),
+ * with x = scale q.K_t, capped by softcap and biased by -alibi_slopes[h] * |p - t|.
+ * Blocks none of whose tokens a row of the chunk attends are not read and their table
+ * entries not looked at.  In the blocks that are read, tokens t < L hidden from some
+ * rows must hold finite V (P = 0 is multiplied with them, as in pkv_paged_prefill);
+ * slots at t >= L may hold anything.
+ * softcap, window, alibi_slopes, prefix_lens: as pkv_paged_attention_decode_scoremod;
+ * everything else, the error bits and the bounded waits included, as pkv_paged_prefill.
+ */
+pkv_status pkv_paged_prefill_scoremod(
+    void* out, const void* query, pkv_dtype q_dtype, const void* key_cache, const void* value_cache,
+    pkv_dtype cache_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* seq_lens, const int32_t* query_start, int num_seqs, int64_t num_query_tokens,
+    int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+    float softcap, int window, const float* alibi_slopes, const int32_t* prefix_lens,
+    pkv_stream_t stream);
 
 /* Size of the static scratch used by pkv_paged_attention_decode_noalloc. */
 #define PKV_STATIC_WORKSPACE_BYTES (16u * 1024u * 1024u)

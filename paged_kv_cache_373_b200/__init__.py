@@ -8,7 +8,7 @@ are not on a CUDA device, the call raises.
 Names follow the C entry points without their ``pkv_`` prefix:
   reshape_and_cache, qk_norm_rope_and_cache, copy_blocks, swap_blocks, paged_attention_decode, paged_prefill,
   paged_attention_decode_noalloc, paged_attention_decode_cascade,
-  paged_attention_decode_scoremod, paged_attention_decode_weights,
+  paged_attention_decode_scoremod, paged_prefill_scoremod, paged_attention_decode_weights,
   paged_attention_weights_workspace_bytes,
   paged_attention_workspace_bytes, default_num_ctas, decode_step_host, decode_step_layout,
   get_device_error, status_string
@@ -37,7 +37,7 @@ EXPORTED = ("pkv_reshape_and_cache", "pkv_qk_norm_rope_and_cache", "pkv_copy_blo
             "pkv_paged_attention_decode_scoremod", "pkv_paged_attention_weights_workspace_bytes",
             "pkv_paged_attention_decode_weights",
             "pkv_paged_attention_decode_noalloc", "pkv_paged_attention_cascade_workspace_bytes",
-            "pkv_paged_attention_decode_cascade", "pkv_paged_prefill", "pkv_decode_step_host",
+            "pkv_paged_attention_decode_cascade", "pkv_paged_prefill", "pkv_paged_prefill_scoremod", "pkv_decode_step_host",
             "pkv_decode_step_layout", "pkv_testing_prefill_timeout",
             "pkv_get_device_error", "pkv_status_string", "pkv_last_error_message")
 
@@ -135,6 +135,8 @@ def lib() -> ctypes.CDLL:
     L.pkv_paged_prefill.restype = c_int
     L.pkv_paged_prefill.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, vp, c_int, i64, c_int,
                                     c_int, c_int, c_int, i64, ctypes.c_float, vp]
+    L.pkv_paged_prefill_scoremod.restype = c_int
+    L.pkv_paged_prefill_scoremod.argtypes = L.pkv_paged_prefill.argtypes[:-1] + [ctypes.c_float, c_int, vp, vp, vp]
     L.pkv_decode_step_host.restype = c_int
     L.pkv_decode_step_host.argtypes = [ctypes.POINTER(DecodeStepArgs), vp]
     L.pkv_decode_step_layout.restype = c_int
@@ -305,6 +307,29 @@ def paged_prefill(out, query, key_cache, value_cache, block_tables, seq_lens, qu
         _dev(out), _dev(query), dtype_code(query), _dev(key_cache), _dev(value_cache),
         dtype_code(key_cache), _dev(block_tables), block_tables.shape[1], _dev(seq_lens),
         _dev(query_start), S, T, Hq, Hkv, D, bs, NB, float(scale), _stream(stream)))
+
+
+def paged_prefill_scoremod(out, query, key_cache, value_cache, block_tables, seq_lens, query_start, scale,
+                           softcap: float = 0.0, window: int = 0, alibi_slopes=None, prefix_lens=None,
+                           stream=None) -> torch.Tensor:
+    """Chunked-prefill attention with modified scores (see paged_attention_decode_scoremod and
+    pkv_paged_prefill_scoremod); query/out [T, Hq, D], rows of sequence s as in paged_prefill."""
+    dev, dt = query.device, query.dtype
+    T, Hq, D = query.shape
+    kc, vc, cdt, (NB, bs, Hkv, cd) = _caches(key_cache, value_cache, dev)
+    S = seq_lens.shape[0]
+    if cd != D or dt not in _DTYPES:
+        raise ValueError("query [T, Hq, D] and the caches disagree")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    _launch(lib().pkv_paged_prefill_scoremod, dev, stream, _arg(out, "out", dev, dt, (T, Hq, D)),
+            _arg(query, "query", dev), _DTYPES[dt], kc, vc, cdt,
+            _arg(block_tables, "block_tables", dev, torch.int32), block_tables.shape[1],
+            _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)),
+            _arg(query_start, "query_start", dev, torch.int32, (S + 1,)), S, T, Hq, Hkv, D, bs, NB, float(scale),
+            float(softcap), int(window), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
+            _arg(prefix_lens, "prefix_lens", dev, torch.int32, (S,)))
+    return out
 
 
 def _pool(t: torch.Tensor) -> int:

@@ -35,6 +35,7 @@
 #include <type_traits>
 
 #include "pkv_device.cuh"
+#include "score_cap.cuh"
 
 namespace pkv {
 
@@ -689,44 +690,6 @@ template <> struct TileInfo<WeightsArg> {
     int nh;
 };
 
-// tanh y, |relative error| < 2^-22: below 1/2 an odd polynomial (a minimax fit
-// of (tanh y) / y - 1 in y^2, off by 1.5e-8 at most), above it
-// 1 - 2 / (1 + e^2|y|) with the hardware's 2^x and reciprocal, whose sum is at
-// least 0.46 there and loses no digits to the subtraction.  y = +-inf gives +-1.
-__device__ __forceinline__ float tanh_poly(float y) {
-    const float z = y * y;
-    float q = fmaf(z, 0.01724149100482464f, -0.05304549261927605f);
-    q = fmaf(z, q, 0.13325878977775574f);
-    q = fmaf(z, q, -0.333331435918808f);
-    return fmaf(y * z, q, y);
-}
-__device__ __forceinline__ float tanh_exp(float y) {
-    const float e = ex2(fabsf(y) * 2.885390081777927f);  // e^(2|y|)
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return copysignf(fmaf(-2.f, r, 1.f), y);
-}
-
-// N scores (log2 domain) capped in place.  Both forms are a select away from
-// each other, so the choice is made per lane for all its scores: the exponential
-// form costs two more of the special-function unit's operations per score.
-template <int N>
-__device__ __forceinline__ void cap_scores(float (&x)[N], const ModArg& m) {
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] *= m.inv_cap2;
-        big = fmaxf(big, fabsf(x[i]));
-    }
-    if (big < 0.5f) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = m.cap2 * tanh_poly(x[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = m.cap2 * (fabsf(x[i]) < 0.5f ? tanh_poly(x[i]) : tanh_exp(x[i]));
-    }
-}
-
 // ---- 16-bit caches (f16 / bf16) and FP8 caches: tensor-core tile math --------
 template <class C>
 struct MmaConsumer {
@@ -871,7 +834,7 @@ struct MmaConsumer {
             x[m][0] = (sa[0] + sb[0]) * sl0; x[m][1] = (sa[1] + sb[1]) * sl1;
             x[m][2] = (sa[2] + sb[2]) * sl0; x[m][3] = (sa[3] + sb[3]) * sl1;
             if constexpr (Arg::kMod) {
-                if (ax.cap2 > 0.f) cap_scores(x[m], ax);
+                if (ax.cap2 > 0.f) cap_scores(x[m], ax.inv_cap2, ax.cap2);
                 if (ti.slopes) {
                     const float d0 = (float)(ti.pos - (ti.tok + 16 * m + gid)), d1 = d0 - 8.f;
                     x[m][0] = fmaf(-sb0, d0, x[m][0]); x[m][1] = fmaf(-sb1, d0, x[m][1]);
@@ -1150,7 +1113,7 @@ struct F32Consumer {
             if constexpr (Arg::kMod) {
                 if (ax.cap2 > 0.f && tok < valid) {
                     float y[1] = {x};
-                    cap_scores(y, ax);
+                    cap_scores(y, ax.inv_cap2, ax.cap2);
                     x = y[0];
                 }
                 if (ti.slopes)

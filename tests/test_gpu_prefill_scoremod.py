@@ -1,0 +1,164 @@
+"""paged_prefill_scoremod on the GPU against fp64 (bounds: scoremod_ref)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_373_b200 as pkv
+from scoremod_ref import assert_near, attend, build, cuda, visible
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def setup(ctx, chunks, Hq, Hkv, D, bs, dtype, seed, window=0, prefixes=None, qscale=1.0):
+    prefixes = prefixes if prefixes is not None else [0] * len(ctx)
+    lens = [a + b for a, b in zip(ctx, chunks)]
+    live = []
+    for c, n, L, pre in zip(ctx, chunks, lens, prefixes):
+        v = np.zeros(L, dtype=bool)
+        for i in range(n):
+            v |= visible(L, c + i, window, pre)
+        # hidden tokens share blocks with attended ones: those hold finite values, whole blocks may hold anything
+        for b in range(0, L, bs):
+            v[b:b + bs] = v[b:b + bs].any()
+        live.append(v)
+    d = cuda(build(lens, Hkv, D, bs, dtype, seed, live))
+    g = torch.Generator().manual_seed(seed + 1)
+    d["q"] = (torch.randn(sum(chunks), Hq, D, generator=g) * qscale).to(dtype).cuda()
+    d["qs"] = torch.tensor([0] + list(np.cumsum(chunks)), dtype=torch.int32).cuda()
+    return d
+
+
+def run(d, scale, **mods):
+    out = torch.full_like(d["q"], 55.0)
+    pkv.paged_prefill_scoremod(out, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], d["qs"], scale, **mods)
+    assert pkv.get_device_error() == 0
+    return out
+
+
+def check(d, out, scale, softcap=0.0, window=0, slopes=None, prefixes=None):
+    qs = d["qs"].tolist()
+    for s, L in enumerate(d["lens"].tolist()):
+        a, b = qs[s], qs[s + 1]
+        if a == b:
+            continue
+        pos = np.arange(a, b) - b + L
+        ref, bound, _, _ = attend(d["q"][a:b].double().cpu().numpy(), d["K"][s], d["V"][s], pos,
+                                  float(np.float32(scale)), d["kc"].dtype, out.dtype, softcap, window,
+                                  None if slopes is None else slopes.double().cpu().numpy(),
+                                  0 if prefixes is None else max(prefixes[s], 0))
+        assert_near(out[a:b], ref, bound, f"sequence {s}, {b - a} rows of {L} tokens")
+
+
+TYPES = [
+    # Hq, Hkv, D, bs, dtype
+    (8, 4, 128, 16, BF16),
+    (4, 4, 64, 32, F16),
+    (16, 2, 64, 16, F16),
+    (16, 1, 128, 32, BF16),
+    (8, 2, 128, 32, F16),
+]
+MODS = [
+    dict(),
+    dict(softcap=3.0),
+    dict(softcap=50.0, window=1),
+    dict(window=16),
+    dict(window=70, alibi=True),
+    dict(alibi=True, softcap=1.5),
+    dict(window=100, prefix=5),
+    dict(window=90, prefix=140, alibi=True, softcap=20.0),
+    dict(window=33, prefix=10000),
+    dict(prefix=230),
+]
+CTX, CHUNKS = [0, 300, 37, 0, 500, 64], [200, 129, 1, 0, 1, 64]
+
+
+@pytest.mark.parametrize("mods", MODS, ids=lambda m: "_".join(f"{k}{v}" for k, v in m.items()) or "plain")
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "%dx%d_D%d_b%d_%s" % (*t[:4], str(t[4])[6:]))
+def test_matches_fp64(types, mods):
+    Hq, Hkv, D, bs, dtype = types
+    mods = dict(mods)
+    prefix = mods.pop("prefix", 0)
+    prefixes = [prefix] * len(CTX) if prefix else None
+    if prefix == 140:
+        prefixes = [140, 17, -3, 5, 64, 0]
+    slopes = torch.linspace(0.02, 0.7, Hq).cuda() if mods.pop("alibi", False) else None
+    d = setup(CTX, CHUNKS, Hq, Hkv, D, bs, dtype, 31, mods.get("window", 0), prefixes, qscale=2.0)
+    pre = None if prefixes is None else torch.tensor(prefixes, dtype=torch.int32).cuda()
+    scale = 1 / D ** 0.5
+    out = run(d, scale, alibi_slopes=slopes, prefix_lens=pre, **mods)
+    check(d, out, scale, slopes=slopes, prefixes=prefixes, **mods)
+
+
+def test_long_context_window_and_sinks():
+    # pairs of units far past the prefix: a long gap, odd and even numbers of units
+    ctx, chunks = [4000, 3333], [300, 77]
+    d = setup(ctx, chunks, 8, 4, 128, 16, BF16, 32, 200, [4, 65])
+    pre = torch.tensor([4, 65], dtype=torch.int32).cuda()
+    out = run(d, 0.09, window=200, prefix_lens=pre)
+    check(d, out, 0.09, 0.0, 200, None, [4, 65])
+    assert (d["tables"] < 0).sum() > 300      # most of the context's blocks were never looked at
+
+
+def test_unmodified_equals_the_plain_prefill():
+    d = setup(CTX, CHUNKS, 8, 4, 64, 16, F16, 33)
+    out = run(d, 0.125)
+    ref = torch.full_like(out, 55.0)
+    pkv.paged_prefill(ref, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], d["qs"], 0.125)
+    check(d, ref, 0.125)
+    check(d, out, 0.125)
+
+
+def test_one_token_chunks_match_the_decode_form():
+    lens = [1, 17, 300, 2049]
+    d = setup([L - 1 for L in lens], [1] * 4, 16, 4, 128, 16, BF16, 34, 150, [10] * 4)
+    pre = torch.full((4,), 10, dtype=torch.int32).cuda()
+    out = run(d, 0.09, window=150, prefix_lens=pre, softcap=4.0)
+    dec = torch.empty_like(out)
+    pkv.paged_attention_decode_scoremod(dec, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], 0.09, window=150,
+                                        prefix_lens=pre, softcap=4.0)
+    check(d, out, 0.09, 4.0, 150, None, [10] * 4)
+    check(d, dec, 0.09, 4.0, 150, None, [10] * 4)
+
+
+def test_large_scores_move_the_reference_on_every_tile():
+    # keys grow along the sequence: each tile's maximum passes the last one's by far more than 2^8
+    d = setup([0, 100], [250, 140], 8, 2, 128, 16, BF16, 35)
+    for s, L in enumerate(d["lens"].tolist()):
+        for t in range(L):
+            b = int(d["tables"][s, t // 16])
+            row = (d["kc"][b, t % 16].float() * (1 + t / 8)).to(BF16)
+            d["kc"][b, t % 16] = row
+            d["K"][s][t] = row.double().cpu().numpy()
+    for cap in (0.0, 30.0):
+        out = run(d, 0.2, softcap=cap)
+        check(d, out, 0.2, cap)
+
+
+def test_errors_are_flagged_and_rows_left():
+    d = setup([10, 20], [5, 5], 8, 4, 64, 16, F16, 36)
+    out = torch.full_like(d["q"], 55.0)
+    short = torch.tensor([3, 25], dtype=torch.int32, device="cuda")
+    pkv.paged_prefill_scoremod(out, d["q"], d["kc"], d["vc"], d["tables"], short, d["qs"], 0.1, window=8)
+    assert pkv.get_device_error() == pkv.DEVERR_SEQ_LEN
+    assert (out[:5] == 55).all()
+    t = d["tables"].clone()
+    t[1, 1] = d["kc"].shape[0] + 3
+    pkv.paged_prefill_scoremod(out, d["q"], d["kc"], d["vc"], t, d["lens"], d["qs"], 0.1, window=8)
+    assert pkv.get_device_error() == pkv.DEVERR_BLOCK_ID
+
+
+def test_graph_replay():
+    d = setup(CTX, CHUNKS, 8, 4, 128, 16, BF16, 37)
+    out = torch.empty_like(d["q"])
+    call = lambda: pkv.paged_prefill_scoremod(out, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], d["qs"], 0.1,
+                                              softcap=9.0)
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    d["q"].mul_(-1)
+    out.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    check(d, out, 0.1, 9.0)
