@@ -16,6 +16,7 @@
  *                              table with the block-wise softmax merge (3.3)
  *   pkv_paged_attention_decode_scoremod  the same with capped, biased or windowed scores
  *   pkv_paged_attention_decode_weights  the same, accumulating each token's attention weight
+ *   pkv_evict_tokens           keep the heaviest and the most recent tokens of a sequence
  *   pkv_paged_attention_decode_cascade  decode with shared prompt prefixes
  *                              read once per group (3.4)
  *   pkv_paged_prefill          chunked-prefill (causal, multi-token) attention
@@ -326,6 +327,46 @@ pkv_status pkv_paged_attention_decode_weights(
     int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
     const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes,
     int num_ctas, pkv_stream_t stream);
+
+/*
+ * pkv_evict_tokens -- cache eviction by accumulated attention weight: shortens
+ * every sequence longer than `budget` tokens to exactly `budget`, per kv head.
+ * For sequence s (L = seq_lens[s]) and kv head h with weights w = weights[s, h, :]
+ * (as pkv_paged_attention_decode_weights accumulates them):
+ *   L > budget: the kept tokens are the last `recent` ones and, of the others, the
+ *     budget - recent of largest w (equal weights: the earlier token first; NaN counts
+ *     as lower than every number), in ascending order t_0 < t_1 < ... < t_{budget-1};
+ *     row t_j of the head's K and V goes to slot j of the sequence's new table,
+ *     block new_block_tables[s][j / block_size], slot j % block_size;
+ *   L <= budget: t_j = j for j < L, and no K/V row is touched (the sequence keeps its
+ *     old table; its new_block_tables row is not looked at);
+ *   n = min(L, budget): new_seq_lens[s] = n, kept[s, h, j] = t_j for j < n and -1 for
+ *     n <= j < budget, new_weights[s, h, j] = w[t_j] for j < n (the rest as it was).
+ * Rows keep their rotary phase, so a rotated K needs no change; different heads of one
+ * slot then hold different tokens, which attention does not mind.
+ * The new blocks must be distinct and must not be blocks that the call reads (the
+ * old blocks, which may be shared with other sequences, are left as they are and can
+ * be released once the stream has passed the call).
+ * weights: DEVICE fp32 [num_seqs, num_kv_heads, weight_len]; new_weights: DEVICE fp32
+ * [num_seqs, num_kv_heads, new_weight_len], not overlapping weights; kept: DEVICE int32
+ * [num_seqs, num_kv_heads, budget]; new_block_tables: DEVICE int32 [num_seqs,
+ * new_max_blocks_per_seq]; new_seq_lens: DEVICE int32 [num_seqs], not seq_lens.
+ * A seq_len below 0, longer than its table row or than weight_len (it is clamped), a
+ * new table shorter than the budget or new_weight_len below n (what does not fit is not
+ * written) sets PKV_DEVERR_SEQ_LEN; a block id out of range (those rows are skipped)
+ * PKV_DEVERR_BLOCK_ID.
+ * cache_dtype f32, f16, bf16 or FP8_E4M3; head_dim in {64, 128}; block_size in {16, 32};
+ * budget > 0; 0 <= recent <= budget.  No workspace; the result is the same bits on
+ * every run.
+ */
+pkv_status pkv_evict_tokens(void* key_cache, void* value_cache, pkv_dtype cache_dtype,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* seq_lens, const float* weights, int64_t weight_len,
+                            const int32_t* new_block_tables, int new_max_blocks_per_seq,
+                            int32_t* new_seq_lens, float* new_weights, int64_t new_weight_len,
+                            int32_t* kept, int budget, int recent, int num_seqs, int num_kv_heads,
+                            int head_dim, int block_size, int64_t num_blocks,
+                            pkv_stream_t stream);
 
 /*
  * pkv_paged_attention_decode_cascade -- decode attention for batches in which

@@ -102,6 +102,20 @@ pkv_status pkv_bm_append_token(pkv_block_manager* bm, int64_t seq_id, int32_t to
 pkv_status pkv_bm_append_batch(pkv_block_manager* bm, const int64_t* seq_ids, const int32_t* tokens,
                                int64_t n, int64_t* slots, int64_t* cow_pairs, int64_t* num_cow);
 
+/* Token eviction (pkv_evict_tokens) for a batch: every sequence seq_ids[i] longer
+ * than `budget` tokens gets ceil(budget / block_size) fresh blocks in place of its
+ * own and from then on has `budget` tokens; the others stay as they are.  Row i
+ * of new_tables[n, new_max_blocks] receives the fresh blocks (padded with -1; all
+ * -1 for a sequence that stays), new_lens[i] the length.  Take the old tables with
+ * pkv_bm_batch_tables first: pkv_evict_tokens copies from them.  All fresh blocks
+ * are taken before any old block is released, so no fresh block is one that the
+ * batch's device call reads; the old ones are released as pkv_bm_free_sequence does
+ * and may be reused by work ordered after that call.  The blocks of a shortened
+ * sequence no longer hold a prompt's prefix: they get no keys, also not the ones it
+ * fills later.  All or nothing: PKV_ENOBLOCKS changes nothing. */
+pkv_status pkv_bm_evict_batch(pkv_block_manager* bm, const int64_t* seq_ids, int64_t n, int64_t budget,
+                              int32_t* new_tables, int64_t new_max_blocks, int32_t* new_lens);
+
 /* Release the sequence; blocks whose count drops to 0 are parked (cached
  * full blocks, tail first) or returned to the free list. */
 pkv_status pkv_bm_free_sequence(pkv_block_manager* bm, int64_t seq_id);

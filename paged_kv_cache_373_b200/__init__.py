@@ -9,7 +9,7 @@ Names follow the C entry points without their ``pkv_`` prefix:
   reshape_and_cache, qk_norm_rope_and_cache, copy_blocks, swap_blocks, paged_attention_decode, paged_prefill,
   paged_attention_decode_noalloc, paged_attention_decode_cascade,
   paged_attention_decode_scoremod, paged_prefill_scoremod, paged_attention_decode_weights,
-  paged_attention_weights_workspace_bytes,
+  paged_attention_weights_workspace_bytes, evict_tokens,
   paged_attention_workspace_bytes, default_num_ctas, decode_step_host, decode_step_layout,
   get_device_error, status_string
 """
@@ -35,7 +35,7 @@ _DTYPES = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_B
 EXPORTED = ("pkv_reshape_and_cache", "pkv_qk_norm_rope_and_cache", "pkv_copy_blocks", "pkv_swap_blocks", "pkv_paged_attention_workspace_bytes",
             "pkv_default_num_ctas", "pkv_paged_attention_decode",
             "pkv_paged_attention_decode_scoremod", "pkv_paged_attention_weights_workspace_bytes",
-            "pkv_paged_attention_decode_weights",
+            "pkv_paged_attention_decode_weights", "pkv_evict_tokens",
             "pkv_paged_attention_decode_noalloc", "pkv_paged_attention_cascade_workspace_bytes",
             "pkv_paged_attention_decode_cascade", "pkv_paged_prefill", "pkv_paged_prefill_scoremod", "pkv_decode_step_host",
             "pkv_decode_step_layout", "pkv_testing_prefill_timeout",
@@ -121,6 +121,9 @@ def lib() -> ctypes.CDLL:
     L.pkv_paged_attention_decode_weights.argtypes = [vp, vp, vp, i64, vp, c_int, vp, vp, c_int, vp, c_int, vp,
                                                      c_int, c_int, c_int, c_int, c_int, i64, ctypes.c_float,
                                                      vp, vp, vp, ctypes.c_size_t, c_int, vp]
+    L.pkv_evict_tokens.restype = c_int
+    L.pkv_evict_tokens.argtypes = [vp, vp, c_int, vp, c_int, vp, vp, i64, vp, c_int, vp, vp, i64, vp, c_int,
+                                   c_int, c_int, c_int, c_int, c_int, i64, vp]
     L.pkv_paged_attention_decode_noalloc.restype = c_int
     L.pkv_paged_attention_decode_noalloc.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp,
                                                      c_int, c_int, c_int, c_int, c_int, i64,
@@ -455,6 +458,30 @@ def paged_attention_decode_weights(out, weights_out, query, key_cache, value_cac
     return out
 
 
+def evict_tokens(key_cache, value_cache, block_tables, seq_lens, weights, new_block_tables, new_seq_lens,
+                 new_weights, kept, budget: int, recent: int, stream=None) -> None:
+    """Shorten every sequence longer than `budget` to its last `recent` and its heaviest other tokens, per
+    kv head, moving their K/V rows to the blocks of new_block_tables (see pkv_evict_tokens).  weights
+    fp32 [S, Hkv, W]; written: new_seq_lens int32 [S], new_weights fp32 [S, Hkv, W'], kept int32
+    [S, Hkv, budget]."""
+    dev = key_cache.device
+    kc, vc, cdt, (NB, bs, Hkv, D) = _caches(key_cache, value_cache, dev)
+    S = seq_lens.shape[0]
+    for x, name in ((weights, "weights"), (new_weights, "new_weights")):
+        if x.dim() != 3 or tuple(x.shape[:2]) != (S, Hkv):
+            raise ValueError(f"{name} must be [num_seqs, num_kv_heads, length]")
+    for x, name in ((block_tables, "block_tables"), (new_block_tables, "new_block_tables")):
+        if x.dim() != 2 or x.shape[0] != S:
+            raise ValueError(f"{name} must be [num_seqs, blocks]")
+    _launch(lib().pkv_evict_tokens, dev, stream, kc, vc, cdt, _arg(block_tables, "block_tables", dev, torch.int32),
+            block_tables.shape[1], _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)),
+            _arg(weights, "weights", dev, torch.float32), weights.shape[2],
+            _arg(new_block_tables, "new_block_tables", dev, torch.int32), new_block_tables.shape[1],
+            _arg(new_seq_lens, "new_seq_lens", dev, torch.int32, (S,)),
+            _arg(new_weights, "new_weights", dev, torch.float32), new_weights.shape[2],
+            _arg(kept, "kept", dev, torch.int32, (S, Hkv, int(budget))), int(budget), int(recent), S, Hkv, D, bs, NB)
+
+
 STATIC_WORKSPACE_BYTES = 16 * 1024 * 1024   # PKV_STATIC_WORKSPACE_BYTES
 
 
@@ -537,7 +564,7 @@ class BmStats(ctypes.Structure):
 
 
 BM_EXPORTED = ("pkv_bm_create", "pkv_bm_destroy", "pkv_bm_add_sequence", "pkv_bm_fork",
-               "pkv_bm_append_token", "pkv_bm_append_batch", "pkv_bm_free_sequence",
+               "pkv_bm_append_token", "pkv_bm_append_batch", "pkv_bm_evict_batch", "pkv_bm_free_sequence",
                "pkv_bm_seq_len", "pkv_bm_block_table", "pkv_bm_batch_tables", "pkv_bm_block_key",
                "pkv_bm_get_stats", "pkv_sha256")
 
@@ -555,6 +582,7 @@ def _bm_lib() -> ctypes.CDLL:
             ("pkv_bm_fork", c_int, [vp, i64, P64]),
             ("pkv_bm_append_token", c_int, [vp, i64, ctypes.c_int32, P64, P64, P64]),
             ("pkv_bm_append_batch", c_int, [vp, vp, vp, i64, vp, vp, P64]),
+            ("pkv_bm_evict_batch", c_int, [vp, vp, i64, i64, vp, i64, vp]),
             ("pkv_bm_free_sequence", c_int, [vp, i64]),
             ("pkv_bm_seq_len", c_int, [vp, i64, P64]),
             ("pkv_bm_block_table", c_int, [vp, i64, vp, i64, P64]),
@@ -631,6 +659,18 @@ class HostBlockManager:
         _check(self._L.pkv_bm_append_batch(self._h, ids.data_ptr(), tok.data_ptr(), n, slots.data_ptr(),
                                            pairs.data_ptr(), ctypes.byref(k)))
         return slots, pairs[:k.value].clone()
+
+    def evict_batch(self, sids, budget: int, new_max_blocks: int = 0):
+        """Fresh blocks for every sequence longer than `budget`, which then holds `budget` tokens (for
+        evict_tokens; take the old tables with batch_tables first): (new_block_tables int32
+        [n, new_max_blocks], rows of -1 for sequences that stay, and new lengths int32 [n])."""
+        new_max_blocks = new_max_blocks or -(-int(budget) // self.block_size)
+        ids = torch.tensor(list(sids), dtype=torch.int64)
+        t = torch.empty((len(sids), new_max_blocks), dtype=torch.int32)
+        lens = torch.empty(len(sids), dtype=torch.int32)
+        _check(self._L.pkv_bm_evict_batch(self._h, ids.data_ptr(), len(sids), int(budget), t.data_ptr(),
+                                          new_max_blocks, lens.data_ptr()))
+        return t, lens
 
     def free_sequence(self, sid: int) -> None:
         _check(self._L.pkv_bm_free_sequence(self._h, sid))

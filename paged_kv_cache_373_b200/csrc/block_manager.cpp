@@ -119,6 +119,7 @@ struct Seq {
     std::vector<int32_t> tokens;
     std::vector<Key> keys;  // keys of the full blocks, in order (prefix cache only)
     std::string extras;
+    bool evicted = false;   // tokens were evicted: its blocks hold no prefix and get no keys
 };
 
 }  // namespace
@@ -224,7 +225,7 @@ struct pkv_block_manager {
             ++cows;
         }
         s.tokens.push_back(token);
-        if (cache && off == bs - 1) {  // the block just filled up
+        if (cache && !s.evicted && off == bs - 1) {  // the block just filled up
             const Key k = key_after(lb > 0 ? &s.keys[lb - 1] : nullptr, s.tokens.data() + lb * bs, s.extras);
             s.keys.push_back(k);
             register_key(s.table[lb], k);
@@ -387,6 +388,48 @@ extern "C" pkv_status pkv_bm_append_batch(pkv_block_manager* bm, const int64_t* 
         if (src >= 0) { cow_pairs[2 * k] = src; cow_pairs[2 * k + 1] = dst; ++k; }
     }
     *num_cow = k;
+    return PKV_OK;
+}
+
+extern "C" pkv_status pkv_bm_evict_batch(pkv_block_manager* bm, const int64_t* seq_ids, int64_t n, int64_t budget,
+                                         int32_t* new_tables, int64_t new_max_blocks, int32_t* new_lens) {
+    if (!bm || n < 0 || budget <= 0 || new_max_blocks <= 0 || (n > 0 && (!seq_ids || !new_tables || !new_lens)))
+        return bm_fail(PKV_EINVAL, "bad argument");
+    const int64_t nblk = (budget - 1) / bm->bs + 1;
+    std::vector<Seq*> ss(n);
+    std::unordered_map<int64_t, int> seen;
+    int64_t need = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        ss[i] = bm->find(seq_ids[i]);
+        if (!ss[i]) return bm_fail(PKV_EINVAL, "unknown sequence %lld", (long long)seq_ids[i]);
+        if (seen[seq_ids[i]]++) return bm_fail(PKV_EINVAL, "sequence %lld twice in one batch", (long long)seq_ids[i]);
+        if ((int64_t)ss[i]->tokens.size() <= budget) continue;
+        if (nblk > new_max_blocks)
+            return bm_fail(PKV_EINVAL, "%lld blocks for the budget > new_max_blocks", (long long)nblk);
+        need += nblk;
+    }
+    if (need > bm->available())
+        return bm_fail(PKV_ENOBLOCKS, "eviction needs %lld blocks, %lld available", (long long)need,
+                       (long long)bm->available());
+    std::vector<std::vector<int32_t>> old(n);
+    for (int64_t i = 0; i < n; ++i) {
+        int32_t* row = new_tables + i * new_max_blocks;
+        std::fill(row, row + new_max_blocks, -1);
+        Seq& s = *ss[i];
+        if ((int64_t)s.tokens.size() > budget) {
+            std::vector<int32_t> fresh(nblk);
+            for (int32_t& b : fresh) b = bm->take();
+            std::copy(fresh.begin(), fresh.end(), row);
+            old[i].swap(s.table);
+            s.table.swap(fresh);
+            s.tokens.resize(budget);  // which tokens stay differs by head: only the count is used
+            s.keys.clear();
+            s.evicted = true;
+        }
+        new_lens[i] = (int32_t)s.tokens.size();
+    }
+    for (const auto& t : old)
+        for (auto b = t.rbegin(); b != t.rend(); ++b) bm->drop(*b);  // tail parked first
     return PKV_OK;
 }
 
