@@ -184,49 +184,64 @@ def dtype_code(t: torch.Tensor) -> int:
     return _DTYPES[t.dtype]
 
 
-def _arg(t: Optional[torch.Tensor], name: str, device: torch.device, dtype=None, shape=None) -> Optional[int]:
-    """Address of a contiguous tensor on `device` (None stays None)."""
+def _refuse(t: torch.Tensor, name: str, index: int, dtype, shape):
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, not {t.device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t: Optional[torch.Tensor], name: str, index: int, dtype=None, shape=None) -> Optional[int]:
+    """Address of a contiguous tensor on CUDA device `index` (None stays None).  One test for all
+    that must hold: these checks are most of a small call's host time."""
     if t is None:
         return None
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device} (a CUDA device), not {t.device}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if (t.get_device() != index or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype)
+            or (shape is not None and t.shape != shape)):
+        _refuse(t, name, index, dtype, shape)
     return t.data_ptr()
 
 
-def _scalar(t: Optional[torch.Tensor], name: str, device: torch.device) -> Optional[int]:
+def _scalar(t: Optional[torch.Tensor], name: str, index: int) -> Optional[int]:
     """Address of a one-element fp32 tensor (an FP8 scale)."""
     if t is not None and t.numel() != 1:
         raise ValueError(f"{name} must have one element")
-    return _arg(t, name, device, torch.float32)
+    return _arg(t, name, index, torch.float32)
 
 
-def _caches(key_cache: torch.Tensor, value_cache: torch.Tensor, device: torch.device):
+def _index(t: torch.Tensor, name: str) -> int:
+    """The CUDA device of a call, from its first tensor."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return i
+
+
+def _caches(key_cache: torch.Tensor, value_cache: torch.Tensor, index: int):
     """(addresses, dtype code, shape) of a K/V pool pair [NB, bs, Hkv, D]."""
-    if key_cache.dim() != 4 or value_cache.dtype != key_cache.dtype:
-        raise ValueError("caches must be [num_blocks, block_size, num_kv_heads, head_dim] of one dtype")
-    shape = tuple(key_cache.shape)
-    if key_cache.dtype not in _DTYPES:
-        raise ValueError(f"cache dtype {key_cache.dtype}")
-    return (_arg(key_cache, "key_cache", device), _arg(value_cache, "value_cache", device, shape=shape),
-            _DTYPES[key_cache.dtype], shape)
+    dt, shape = key_cache.dtype, key_cache.shape
+    if len(shape) != 4 or dt not in _DTYPES:
+        raise ValueError("caches must be [num_blocks, block_size, num_kv_heads, head_dim] of a supported dtype")
+    return (_arg(key_cache, "key_cache", index), _arg(value_cache, "value_cache", index, dt, shape), _DTYPES[dt],
+            shape)
 
 
-def _launch(fn, device: torch.device, stream, *args) -> None:
-    """Call a library function with `device` current, on `stream` (default: its current one)."""
+def _launch(fn, index: int, stream, *args) -> None:
+    """Call a library function with CUDA device `index` current, on `stream` (default: its current one)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, s))
+        s = torch._C._cuda_getCurrentRawStream(index)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, s))
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch.cuda.current_device():
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, s)
+    if st:
+        _check(st)
 
 
 def status_string(status: int) -> str:
@@ -251,33 +266,33 @@ def qk_norm_rope_and_cache(query_out, query, key, value, key_cache, value_cache,
     [max_position, rotary_dim] is given), write q to query_out and k, v to their cache slots.
     query [T, Hq, D], key/value [T, Hkv, D]: heads contiguous, any token stride
     (see pkv_qk_norm_rope_and_cache)."""
-    dev, dt = query.device, query.dtype
-    T, Hq, D = query.shape
-    Hkv = key.shape[1]
-    kc, vc, cdt, (NB, bs, chkv, cd) = _caches(key_cache, value_cache, dev)
-    if tuple(key.shape) != (T, Hkv, D) or value.shape != key.shape or (chkv, cd) != (Hkv, D):
+    dev, dt = _index(query, "query"), query.dtype
+    qshape = query.shape
+    T, Hq, D = qshape
+    kc, vc, cdt, (NB, bs, Hkv, cd) = _caches(key_cache, value_cache, dev)
+    if key.shape != (T, Hkv, D) or value.shape != key.shape or cd != D:
         raise ValueError("query [T, Hq, D], key and value [T, Hkv, D] and the caches disagree")
-    if dt not in (torch.float32, torch.float16, torch.bfloat16):
+    if dt not in _DTYPES:
         raise ValueError(f"query dtype {dt}")
     ptrs = []
-    for x, name in ((query, "query"), (key, "key"), (value, "value")):
-        if x.device != dev or x.dtype != dt or not x.is_cuda:
-            raise ValueError(f"{name} must be {dt} on {dev} (a CUDA device)")
-        h = x.shape[1]
-        if (x.stride(2) != 1 and D > 1) or (h > 1 and x.stride(1) != D):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-        ptrs += [x.data_ptr(), x.stride(0) if T > 1 else h * D]
+    for x, h in ((query, Hq), (key, Hkv), (value, Hkv)):
+        t_stride, h_stride, d_stride = x.stride()
+        if x.get_device() != dev or x.dtype is not dt:
+            raise ValueError(f"query, key and value must be {dt} on CUDA device {dev}")
+        if d_stride != 1 or (h > 1 and h_stride != D):
+            raise ValueError("query, key, value: the heads of a token must be contiguous")
+        ptrs += (x.data_ptr(), t_stride if T > 1 else h * D)
     rot, max_pos, table = 0, 0, None
     if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [max_position, rotary_dim]")
+        if cos_sin.dim() != 2 or positions is None:
+            raise ValueError("cos_sin must be [max_position, rotary_dim], with positions")
         max_pos, rot = cos_sin.shape
         table = _arg(cos_sin, "cos_sin", dev, torch.float32)
         positions = _arg(positions, "positions", dev, torch.int64, (T,))
     else:
         positions = None
     _launch(lib().pkv_qk_norm_rope_and_cache, dev, stream,
-            _arg(query_out, "query_out", dev, dt, (T, Hq, D)), *ptrs, _DTYPES[dt], kc, vc, cdt,
+            _arg(query_out, "query_out", dev, dt, qshape), *ptrs, _DTYPES[dt], kc, vc, cdt,
             _arg(slot_mapping, "slot_mapping", dev, torch.int64, (T,)), positions, table, max_pos, rot,
             int(bool(interleaved)), _arg(q_weight, "q_weight", dev, dt, (D,)),
             _arg(k_weight, "k_weight", dev, dt, (D,)), float(eps), T, NB, bs, Hq, Hkv, D,
@@ -317,17 +332,18 @@ def paged_prefill_scoremod(out, query, key_cache, value_cache, block_tables, seq
                            stream=None) -> torch.Tensor:
     """Chunked-prefill attention with modified scores (see paged_attention_decode_scoremod and
     pkv_paged_prefill_scoremod); query/out [T, Hq, D], rows of sequence s as in paged_prefill."""
-    dev, dt = query.device, query.dtype
-    T, Hq, D = query.shape
+    dev, dt, shape = _index(query, "query"), query.dtype, query.shape
+    T, Hq, D = shape
     kc, vc, cdt, (NB, bs, Hkv, cd) = _caches(key_cache, value_cache, dev)
     S = seq_lens.shape[0]
     if cd != D or dt not in _DTYPES:
         raise ValueError("query [T, Hq, D] and the caches disagree")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+    tshape = block_tables.shape
+    if len(tshape) != 2 or tshape[0] != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    _launch(lib().pkv_paged_prefill_scoremod, dev, stream, _arg(out, "out", dev, dt, (T, Hq, D)),
+    _launch(lib().pkv_paged_prefill_scoremod, dev, stream, _arg(out, "out", dev, dt, shape),
             _arg(query, "query", dev), _DTYPES[dt], kc, vc, cdt,
-            _arg(block_tables, "block_tables", dev, torch.int32), block_tables.shape[1],
+            _arg(block_tables, "block_tables", dev, torch.int32), tshape[1],
             _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)),
             _arg(query_start, "query_start", dev, torch.int32, (S + 1,)), S, T, Hq, Hkv, D, bs, NB, float(scale),
             float(softcap), int(window), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
@@ -400,18 +416,18 @@ def paged_attention_decode(out, query, key_cache, value_cache, block_tables, seq
 
 
 def _decode_args(out, query, key_cache, value_cache, block_tables, seq_lens):
-    """The arguments a decode call shares, checked: (device, shape, leading arguments)."""
-    dev, dt = query.device, query.dtype
-    S, Hq, D = query.shape
+    """What a decode call's arguments share, checked: (device, sizes, address of out, leading arguments)."""
+    dev, dt, shape, tshape = _index(query, "query"), query.dtype, query.shape, block_tables.shape
+    S, Hq, D = shape
     kc, vc, cdt, (NB, bs, Hkv, cd) = _caches(key_cache, value_cache, dev)
     if cd != D or dt not in _DTYPES:
         raise ValueError("query [S, Hq, D] and the caches disagree")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if len(tshape) != 2 or tshape[0] != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
     args = (_arg(query, "query", dev), _DTYPES[dt], kc, vc, cdt,
-            _arg(block_tables, "block_tables", dev, torch.int32), block_tables.shape[1],
+            _arg(block_tables, "block_tables", dev, torch.int32), tshape[1],
             _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)), S, Hq, Hkv, D, bs, NB)
-    return dev, (S, Hq, Hkv, D, block_tables.shape[1] * bs), _arg(out, "out", dev, dt, (S, Hq, D)), args
+    return dev, (S, Hq, Hkv, D, tshape[1] * bs), _arg(out, "out", dev, dt, shape), args
 
 
 def paged_attention_decode_scoremod(out, query, key_cache, value_cache, block_tables, seq_lens, scale,
@@ -423,7 +439,8 @@ def paged_attention_decode_scoremod(out, query, key_cache, value_cache, block_ta
     prefix_lens[s] (int32 [S]) (see pkv_paged_attention_decode_scoremod)."""
     dev, (S, Hq, Hkv, D, _), o, args = _decode_args(out, query, key_cache, value_cache, block_tables, seq_lens)
     if workspace is None:
-        workspace = alloc_workspace(S, Hq, Hkv, D, num_ctas, device=dev)
+        with torch.cuda.device(dev):
+            workspace = alloc_workspace(S, Hq, Hkv, D, num_ctas, device=query.device)
     _launch(lib().pkv_paged_attention_decode_scoremod, dev, stream, o, *args, float(scale), float(softcap),
             int(window), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
             _arg(prefix_lens, "prefix_lens", dev, torch.int32, (S,)), _scalar(k_scale, "k_scale", dev),
@@ -444,15 +461,16 @@ def paged_attention_decode_weights(out, weights_out, query, key_cache, value_cac
     kv head) to `weights` (fp32 [S, Hkv, weight_len], None: zeros) and stores it in weights_out, which
     may be `weights` (see pkv_paged_attention_decode_weights)."""
     dev, (S, Hq, Hkv, D, cap), o, args = _decode_args(out, query, key_cache, value_cache, block_tables, seq_lens)
-    if weights_out.dim() != 3 or tuple(weights_out.shape[:2]) != (S, Hkv):
+    wshape = weights_out.shape
+    if len(wshape) != 3 or wshape[0] != S or wshape[1] != Hkv:
         raise ValueError("weights_out must be [num_seqs, num_kv_heads, weight_len]")
     wo = _arg(weights_out, "weights_out", dev, torch.float32)
-    wi = _arg(weights, "weights", dev, torch.float32, tuple(weights_out.shape))
+    wi = _arg(weights, "weights", dev, torch.float32, wshape)
     if workspace is None:
         with torch.cuda.device(dev):
             n = paged_attention_weights_workspace_bytes(S, Hq, Hkv, D, cap, num_ctas)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-    _launch(lib().pkv_paged_attention_decode_weights, dev, stream, o, wo, wi, weights_out.shape[2], *args,
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=query.device)
+    _launch(lib().pkv_paged_attention_decode_weights, dev, stream, o, wo, wi, wshape[2], *args,
             float(scale), _scalar(k_scale, "k_scale", dev), _scalar(v_scale, "v_scale", dev),
             _arg(workspace, "workspace", dev), workspace.nbytes, int(num_ctas))
     return out
@@ -464,21 +482,20 @@ def evict_tokens(key_cache, value_cache, block_tables, seq_lens, weights, new_bl
     kv head, moving their K/V rows to the blocks of new_block_tables (see pkv_evict_tokens).  weights
     fp32 [S, Hkv, W]; written: new_seq_lens int32 [S], new_weights fp32 [S, Hkv, W'], kept int32
     [S, Hkv, budget]."""
-    dev = key_cache.device
+    dev = _index(key_cache, "key_cache")
     kc, vc, cdt, (NB, bs, Hkv, D) = _caches(key_cache, value_cache, dev)
     S = seq_lens.shape[0]
-    for x, name in ((weights, "weights"), (new_weights, "new_weights")):
-        if x.dim() != 3 or tuple(x.shape[:2]) != (S, Hkv):
-            raise ValueError(f"{name} must be [num_seqs, num_kv_heads, length]")
-    for x, name in ((block_tables, "block_tables"), (new_block_tables, "new_block_tables")):
-        if x.dim() != 2 or x.shape[0] != S:
-            raise ValueError(f"{name} must be [num_seqs, blocks]")
+    ws, nws, ts, nts = weights.shape, new_weights.shape, block_tables.shape, new_block_tables.shape
+    if len(ws) != 3 or len(nws) != 3 or ws[:2] != (S, Hkv) or nws[:2] != (S, Hkv):
+        raise ValueError("weights and new_weights must be [num_seqs, num_kv_heads, length]")
+    if len(ts) != 2 or len(nts) != 2 or ts[0] != S or nts[0] != S:
+        raise ValueError("block_tables and new_block_tables must be [num_seqs, blocks]")
     _launch(lib().pkv_evict_tokens, dev, stream, kc, vc, cdt, _arg(block_tables, "block_tables", dev, torch.int32),
-            block_tables.shape[1], _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)),
-            _arg(weights, "weights", dev, torch.float32), weights.shape[2],
-            _arg(new_block_tables, "new_block_tables", dev, torch.int32), new_block_tables.shape[1],
+            ts[1], _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)),
+            _arg(weights, "weights", dev, torch.float32), ws[2],
+            _arg(new_block_tables, "new_block_tables", dev, torch.int32), nts[1],
             _arg(new_seq_lens, "new_seq_lens", dev, torch.int32, (S,)),
-            _arg(new_weights, "new_weights", dev, torch.float32), new_weights.shape[2],
+            _arg(new_weights, "new_weights", dev, torch.float32), nws[2],
             _arg(kept, "kept", dev, torch.int32, (S, Hkv, int(budget))), int(budget), int(recent), S, Hkv, D, bs, NB)
 
 

@@ -71,6 +71,24 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_
     // whose length scan takes more than two rounds of a warp, 8 boundaries
     // per CTA located by one CTA-wide scan
     const bool wide = p.num_seqs > 2 * 32 * kScanPerLane;
+    if constexpr (Arg::kMod || Arg::kWeights) {
+        // small batches of the variants: a CTA per unit (see pkv_merge_units_kernel)
+        const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nch;
+        if (p.num_seqs <= 32 * kScanPerLane && units <= workers) {
+            cudaLaunchAttribute pdl[1];
+            pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            pdl[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.gridDim = dim3((unsigned)units);
+            cfg.blockDim = dim3(kUnitWarps * 32);
+            cfg.stream = st;
+            cfg.attrs = pdl;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, pkv_merge_units_kernel<typename C::q_t, C::D, C::kTT, Arg>, p, workers, sx);
+            if (e == cudaSuccess) e = cudaGetLastError();
+            if (e != cudaSuccess) return fail(PKV_ECUDA, "merge launch: %s", cudaGetErrorString(e));
+            return PKV_OK;
+        }
+    }
     cfg.gridDim = dim3((unsigned)(wide ? (workers + kMergeWarps - 1) / kMergeWarps : workers));
     cfg.blockDim = dim3(32 * (wide ? kMergeWarps : p.hpu));
     cfg.dynamicSmemBytes = 0;

@@ -6,11 +6,10 @@
 // Two kernels.
 //   select: one CTA per (sequence, kv head) finds the budget's threshold by radix
 //     selection on the weights' bits (11 + 11 + 10 bits, a shared-memory histogram
-//     a pass), then numbers the kept tokens in order: each warp counts its
-//     contiguous share by ballots, one scan over the warps, and the share is walked
-//     again.  Integer work only, so the result does not depend on any order.
-//     Bound: the latency of four passes over one row of weights (from L2 after
-//     the first).
+//     a pass), then numbers the kept tokens in order by ballots and one scan.  A row
+//     of up to 16384 weights is loaded once and stays in registers (a longer one is
+//     read again each pass).  Integer work only, so the result does not depend on
+//     any order.  Bound: the latency of its barriers and shared-memory atomics.
 //   gather: one CTA per destination block copies its rows, 16 bytes per thread and
 //     access, K and V in flight together.  Bound: memory -- every kept row is read
 //     and written once; a row is at least one 64-byte run.
@@ -39,6 +38,9 @@ struct EvictParams {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kKeys = 16;                           // weights a thread holds
+constexpr int kBatch = kSelThreads * kKeys;         // tokens the CTA holds at once
+constexpr int kRuns = kSelWarps * kKeys;            // runs of 32 neighbouring tokens in a batch
 
 // Order-preserving map of a weight to an unsigned key; NaN is the lowest, -0 is +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -63,7 +65,7 @@ evict_select_kernel(const EvictParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int hist[kBins];
     __shared__ int wsum[kSelWarps];
-    __shared__ int gt_before[kSelWarps], eq_before[kSelWarps];
+    __shared__ int run_gt[kRuns], run_eq[kRuns];
     __shared__ uint32_t sh_digit;
     __shared__ int sh_left;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,6 +96,22 @@ evict_select_kernel(const EvictParams p) {
     for (int t = m + tid; t < L; t += kSelThreads) keep(c + t - m, t);
     if (c == 0) return;
 
+    // the weights of a batch, all loads in flight; a row that fits one batch is
+    // loaded once and stays in registers through the passes
+    uint32_t key[kKeys];
+    auto load = [&](int base) {
+        float x[kKeys];
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int t = base + i * kSelThreads + tid;
+            x[i] = t < m ? w[t] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) key[i] = weight_key(x[i]);
+    };
+    const bool one = m <= kBatch;
+    if (one) load(0);
+
     // ---- the c-th largest key: digit by digit from the top
     uint32_t prefix = 0;
     int left = c;  // rank still to find among the keys that share the prefix
@@ -103,9 +121,14 @@ evict_select_kernel(const EvictParams p) {
         for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
         __syncthreads();
         const uint32_t mask = d == 0 ? 0u : 0xffffffffu << (kShift[d] + kBits[d]);
-        for (int t = tid; t < m; t += kSelThreads) {
-            const uint32_t k = weight_key(w[t]);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> kShift[d]) & ((1u << kBits[d]) - 1)], 1);
+        for (int base = 0; base < m; base += kBatch) {
+            if (!one) load(base);
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                const uint32_t k = key[i];
+                if (base + i * kSelThreads + tid < m && (k & mask) == prefix)
+                    atomicAdd(&hist[(k >> kShift[d]) & ((1u << kBits[d]) - 1)], 1);
+            }
         }
         __syncthreads();
         // thread i holds bins kBins-1-2i and kBins-2-2i: counts from the top down
@@ -141,46 +164,58 @@ evict_select_kernel(const EvictParams p) {
     }
     // every key above `prefix` stays, and the first `left` of those equal to it
 
-    // ---- number the kept tokens in order
-    const int share = (m + kSelThreads - 1) / kSelThreads * 32;  // tokens per warp
-    const int b0 = min(m, warp * share), b1 = min(m, b0 + share);
-    int gt = 0, eq = 0;
-    for (int t0 = b0; t0 < b1; t0 += 32) {
-        const int t = t0 + lane;
-        const uint32_t k = t < b1 ? weight_key(w[t]) : 0u;
-        gt += __popc(__ballot_sync(kFull, t < b1 && k > prefix));
-        eq += __popc(__ballot_sync(kFull, t < b1 && k == prefix));
-    }
-    if (lane == 0) {
-        gt_before[warp] = gt;
-        eq_before[warp] = eq;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        const int vg = gt_before[lane], ve = eq_before[lane];
-        int g = vg, e = ve;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int yg = __shfl_up_sync(kFull, g, o), ye = __shfl_up_sync(kFull, e, o);
-            if (lane >= o) { g += yg; e += ye; }
-        }
-        gt_before[lane] = g - vg;
-        eq_before[lane] = e - ve;
-    }
-    __syncthreads();
-    gt = gt_before[warp];
-    eq = eq_before[warp];
+    // ---- number the kept tokens in order: the ballots of a batch's runs of 32
+    // tokens (run i * kSelWarps + warp), a scan over the runs, and the totals so far
+    int gt0 = 0, eq0 = 0;
     const unsigned below = (1u << lane) - 1;
-    for (int t0 = b0; t0 < b1; t0 += 32) {
-        const int t = t0 + lane;
-        const uint32_t k = t < b1 ? weight_key(w[t]) : 0u;
-        const unsigned bg = __ballot_sync(kFull, t < b1 && k > prefix);
-        const unsigned be = __ballot_sync(kFull, t < b1 && k == prefix);
-        const int g = gt + __popc(bg & below), e = eq + __popc(be & below);
-        const bool is_gt = (bg >> lane) & 1, is_eq = (be >> lane) & 1;
-        if (is_gt || (is_eq && e < left)) keep(g + min(e, left), t);
-        gt += __popc(bg);
-        eq += __popc(be);
+    for (int base = 0; base < m; base += kBatch) {
+        if (!one) load(base);
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const bool in = base + i * kSelThreads + tid < m;
+            const unsigned bg = __ballot_sync(kFull, in && key[i] > prefix);
+            const unsigned be = __ballot_sync(kFull, in && key[i] == prefix);
+            if (lane == 0) {
+                run_gt[i * kSelWarps + warp] = __popc(bg);
+                run_eq[i * kSelWarps + warp] = __popc(be);
+            }
+        }
+        __syncthreads();
+        if (warp < 2) {  // exclusive scan of kRuns counts, kKeys per lane; warp 0: gt, warp 1: eq
+            int* run = warp ? run_eq : run_gt;
+            int v[kKeys], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                v[i] = run[lane * kKeys + i];
+                sum += v[i];
+            }
+            int x = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) wsum[warp] = x;
+            x -= sum;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                run[lane * kKeys + i] = x;
+                x += v[i];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int t = base + i * kSelThreads + tid;
+            const bool is_gt = t < m && key[i] > prefix, is_eq = t < m && key[i] == prefix;
+            const unsigned bg = __ballot_sync(kFull, is_gt), be = __ballot_sync(kFull, is_eq);
+            const int g = gt0 + run_gt[i * kSelWarps + warp] + __popc(bg & below);
+            const int e = eq0 + run_eq[i * kSelWarps + warp] + __popc(be & below);
+            if (is_gt || (is_eq && e < left)) keep(g + min(e, left), t);
+        }
+        gt0 += wsum[0];
+        eq0 += wsum[1];
+        __syncthreads();
     }
 }
 

@@ -30,11 +30,15 @@ namespace {
 //   w = sum over the group's q heads of 2^(score - lse),
 //   out[t] = in[t] + w  (t < L - 1),   out[L - 1] = w  (the step's own token).
 // One thread owns a token, so the sum has one order and nothing is atomic.
-// Items of kWeightTokens tokens are dealt to a persistent grid; scores come
-// mostly from L2, where the decode pass has just written them.
+// The items (runs of kWeightTokens tokens of a sequence and kv head) are laid
+// end to end and every CTA takes an equal share; it finds its first one while
+// the decode pass still runs.  Scores come mostly from L2, where that pass has
+// just written them: bound by their latency, so kWeightHeads heads' loads of
+// every token are in flight together.
 // ----------------------------------------------------------------------------
-constexpr int kWeightThreads = 256, kWeightPer = 4;  // tokens per thread
+constexpr int kWeightThreads = 256, kWeightPer = 2;  // tokens per thread
 constexpr int kWeightTokens = kWeightThreads * kWeightPer;
+constexpr int kWeightHeads = 4;
 
 struct WeightsOut {
     const float* in;  // [num_seqs, num_kv_heads, len] or null (zeros)
@@ -45,43 +49,46 @@ struct WeightsOut {
 __global__ void __launch_bounds__(kWeightThreads)
 pkv_weights_kernel(const DecodeParams p, const WeightsArg a, const WeightsOut w) {
     const WaitPrimaryAtExit<true> wait_at_exit;
-    const int cap = p.max_blocks_per_seq * p.block_size;
-    const int chunks = (cap + kWeightTokens - 1) / kWeightTokens;
-    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads * chunks;
-    bool waited = false;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t u = it / chunks;  // sequence * num_kv_heads + kv head
-        const int s = (int)(u / p.num_kv_heads), kh = (int)(u % p.num_kv_heads);
-        const int t0 = (int)(it % chunks) * kWeightTokens;
-        int L = clamp_len(__ldg(p.seq_lens + s), cap);
-        if (L > w.len) {
-            if (threadIdx.x == 0 && t0 == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
-        }
+    const Lens<false> ln{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq * p.block_size};
+    const int64_t W = total_tiles<kWeightTokens>(ln);
+    const int64_t share = (W + gridDim.x - 1) / gridDim.x;
+    const int64_t tb = min(W, blockIdx.x * share), te = min(W, tb + share);
+    if (tb >= te) return;
+    Walk<kWeightTokens> walk;
+    walk.init(ln, tb, te);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (; !walk.done; walk.advance(ln)) {
+        const int s = walk.s, kh = walk.j, L = walk.L, t0 = walk.i * kWeightTokens + threadIdx.x;
+        if (L > w.len && walk.i == 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
         const int n = (int)min((int64_t)L, w.len);
-        if (t0 >= n) continue;
-        if (!waited) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            waited = true;
-        }
         const int64_t row0 = (int64_t)s * p.num_heads + (int64_t)kh * p.g;
-        float acc[kWeightPer] = {};
-        for (int h = 0; h < p.g; ++h) {
-            const float lse = a.lse[row0 + h];
-            const float* sc = a.scores + (row0 + h) * a.stride + t0 + threadIdx.x;
-            float x[kWeightPer];
-#pragma unroll
-            for (int k = 0; k < kWeightPer; ++k)
-                x[k] = t0 + threadIdx.x + k * kWeightThreads < n ? sc[k * kWeightThreads] : -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kWeightPer; ++k) acc[k] += ex2(x[k] - lse);
-        }
+        const int64_t at = ((int64_t)s * p.num_kv_heads + kh) * w.len + t0;
+        float old[kWeightPer], acc[kWeightPer];
 #pragma unroll
         for (int k = 0; k < kWeightPer; ++k) {
-            const int t = t0 + threadIdx.x + k * kWeightThreads;
-            if (t >= n) continue;
-            const int64_t at = u * w.len + t;
-            w.out[at] = (w.in && t < L - 1 ? w.in[at] : 0.f) + acc[k];
+            const int t = t0 + k * kWeightThreads;
+            old[k] = w.in && t < n && t < L - 1 ? w.in[at + k * kWeightThreads] : 0.f;
+            acc[k] = 0.f;
         }
+        for (int h0 = 0; h0 < p.g; h0 += kWeightHeads) {
+            float x[kWeightHeads][kWeightPer], lse[kWeightHeads];
+#pragma unroll
+            for (int i = 0; i < kWeightHeads; ++i) {
+                const bool on = h0 + i < p.g;
+                lse[i] = on ? a.lse[row0 + h0 + i] : 0.f;
+                const float* sc = a.scores + (row0 + h0 + i) * a.stride + t0;
+#pragma unroll
+                for (int k = 0; k < kWeightPer; ++k)
+                    x[i][k] = on && t0 + k * kWeightThreads < n ? sc[k * kWeightThreads] : -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < kWeightHeads; ++i)
+#pragma unroll
+                for (int k = 0; k < kWeightPer; ++k) acc[k] += ex2(x[i][k] - lse[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < kWeightPer; ++k)
+            if (t0 + k * kWeightThreads < n) w.out[at + k * kWeightThreads] = old[k] + acc[k];
     }
 }
 

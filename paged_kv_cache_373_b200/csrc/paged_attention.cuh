@@ -1748,4 +1748,110 @@ pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
     }
 }
 
+// ----------------------------------------------------------------------------
+// The same merge for the decode variants on small batches (one round of the
+// length scan covers the batch, no more units than workers): there a unit is
+// cut into many segments -- a 777-token sequence alone on the GPU into 49 -- and
+// a warp folding them four at a time is most of a small call's time.  A CTA
+// per unit; its 8 warps share the heads' segments (part k of a head takes every
+// kParts-th), each with kFold segments' loads in flight, and the parts are
+// combined through shared memory.  The order is fixed by the split alone.
+// ----------------------------------------------------------------------------
+constexpr int kUnitWarps = 8, kFold = 8;
+template <typename QT, int D, int TT, class Arg>
+__global__ void __launch_bounds__(kUnitWarps * 32)
+pkv_merge_units_kernel(const DecodeParams p, int64_t workers, const Arg ax) {
+    const WaitPrimaryAtExit<Arg::kWeights> wait_at_exit;
+    if constexpr (Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int PER = D / 32;
+    __shared__ float part_o[kUnitWarps][D];
+    __shared__ float2 part_ml[kUnitWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const auto ln = make_lens<TT>(p, ax);
+    const int s = (int)(blockIdx.x / ln.units), j = (int)(blockIdx.x % ln.units);
+    int64_t W, base;
+    seq_tile_base<TT>(ln, s, &W, &base);
+    const int nt = ntiles_of<TT>(ln.eff(s));
+    const int kh = j / p.nch, c = j % p.nch;
+    const int nh = min(kHeadsPerUnit, p.g - kHeadsPerUnit * c);
+    const int64_t row0 = (int64_t)s * p.num_heads + (int64_t)kh * p.g + kHeadsPerUnit * c;
+    QT* out = reinterpret_cast<QT*>(p.out) + row0 * D;
+    if (nt == 0) {  // nothing to attend
+        for (int i = threadIdx.x; i < nh * D; i += kUnitWarps * 32) out[i] = from_f32<QT>(0.f);
+        return;
+    }
+    const int64_t chunk = (W + workers - 1) / workers;
+    const int64_t T0 = base + (int64_t)j * nt;
+    const int64_t bf = T0 / chunk, bl = (T0 + nt - 1) / chunk;
+    if (bf == bl) return;  // one worker had the whole unit
+    const int parts = kUnitWarps / nh;
+    const int h = warp % nh, part = warp / nh;
+    const int64_t u = ((int64_t)s * p.num_kv_heads + kh) * p.nch + c;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float M = -INFINITY, ls = 0.f, o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    if (part < parts) {
+        for (int64_t w0 = bf + part; w0 <= bl; w0 += kFold * parts) {
+            float2 ml[kFold];
+            float v[kFold][PER];
+#pragma unroll
+            for (int k = 0; k < kFold; ++k) {
+                const int64_t w = w0 + k * parts;
+                ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) v[k][e] = 0.f;
+                if (w <= bl) {
+                    ml[k] = p.ws_ml[(w + u) * p.hpu + h];
+                    const float* src = p.ws_o + ((w + u) * p.hpu + h) * D;
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) v[k][e] = src[lane + 32 * e];
+                }
+            }
+            float Mb = M;
+#pragma unroll
+            for (int k = 0; k < kFold; ++k) Mb = fmaxf(Mb, ml[k].x);
+            if (Mb == -INFINITY) continue;  // nothing attended yet
+            const float fo = ex2(M - Mb);
+            ls *= fo;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] *= fo;
+#pragma unroll
+            for (int k = 0; k < kFold; ++k) {
+                const float f = ex2(ml[k].x - Mb);
+                ls += ml[k].y * f;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) o[e] += v[k][e] * f;
+            }
+            M = Mb;
+        }
+    }
+    if (parts > 1) {
+        if (lane == 0) part_ml[warp] = make_float2(M, ls);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) part_o[warp][lane + 32 * e] = o[e];
+        __syncthreads();
+        if (part > 0) return;
+        float Mb = M;
+        for (int k = 1; k < parts; ++k) Mb = fmaxf(Mb, part_ml[h + k * nh].x);
+        const float fo = M == -INFINITY ? 0.f : ex2(M - Mb);
+        ls *= fo;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] *= fo;
+        for (int k = 1; k < parts; ++k) {
+            const float2 ml = part_ml[h + k * nh];
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mb);
+            ls += ml.y * f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] += part_o[h + k * nh][lane + 32 * e] * f;
+        }
+        M = Mb;
+    }
+    if (part > 0) return;
+    if constexpr (Arg::kWeights)
+        if (lane == 0) ax.lse[row0 + h] = M + log2f(ls);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) out[h * D + lane + 32 * e] = from_f32<QT>(ls > 0.f ? o[e] / ls : 0.f);
+}
+
 }  // namespace pkv
