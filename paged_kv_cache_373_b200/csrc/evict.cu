@@ -4,14 +4,15 @@
 // rows move to the first `budget` slots of a new block table.
 //
 // Two kernels.
-//   select: one CTA per (sequence, kv head) finds the budget's threshold by radix
-//     selection on the weights' bits (11 + 11 + 10 bits, a shared-memory histogram
-//     a pass), then numbers the kept tokens in order by ballots and one scan.  A row
-//     of up to 16384 weights is loaded once and stays in registers (a longer one is
-//     read again each pass).  Integer work only, so the result does not depend on
-//     any order.  Bound: the latency of its barriers and shared-memory atomics.
+//   select: one CTA per (sequence, kv head) finds the budget's threshold on the
+//     weights' bits, then numbers the kept tokens in order by ballots and one scan.
+//     Integer work only, so the result does not depend on any order.  A row of up to
+//     kBatch weights is loaded once, stays in registers and is searched bit by bit
+//     (at most 33 counts); a longer one is read again for each of three histograms
+//     (11 + 11 + 10 bits) and once more for the numbering.  Bound: the latency of
+//     its barriers.
 //   gather: one CTA per destination block copies its rows, 16 bytes per thread and
-//     access, K and V in flight together.  Bound: memory -- every kept row is read
+//     access, K and V of four rows in flight together.  Bound: memory -- every kept row is read
 //     and written once; a row is at least one 64-byte run.
 // The source and the destination are different blocks, so nothing is moved onto
 // rows still to be read, blocks shared with other sequences stay as they are, and
@@ -36,7 +37,7 @@ struct EvictParams {
     int num_seqs, hkv, mbps, new_mbps, bs, budget, recent, row_bytes;
 };
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeys = 16;                           // weights a thread holds
 constexpr int kBatch = kSelThreads * kKeys;         // tokens the CTA holds at once
@@ -60,12 +61,13 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int s, bool* bad)
     return L;
 }
 
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 2)
 evict_select_kernel(const EvictParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int hist[kBins];
     __shared__ int wsum[kSelWarps];
     __shared__ int run_gt[kRuns], run_eq[kRuns];
+    __shared__ int count[2][kSelWarps];
     __shared__ uint32_t sh_digit;
     __shared__ int sh_left;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -81,6 +83,7 @@ evict_select_kernel(const EvictParams p) {
     float* nw = p.new_weights + u * p.new_weight_len;
     int32_t* kept = p.kept + u * p.budget;
     auto keep = [&](int j, int t) {
+        if (j >= p.budget) return;
         kept[j] = t;
         if (j < p.new_weight_len) nw[j] = w[t];
     };
@@ -103,64 +106,98 @@ evict_select_kernel(const EvictParams p) {
         float x[kKeys];
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
+            if (base + i * kSelThreads >= m) break;  // (the same for every thread, here and below)
             const int t = base + i * kSelThreads + tid;
             x[i] = t < m ? w[t] : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) key[i] = weight_key(x[i]);
+        for (int i = 0; i < kKeys; ++i) {
+            if (base + i * kSelThreads >= m) break;
+            key[i] = base + i * kSelThreads + tid < m ? weight_key(x[i]) : 0u;  // 0: below every candidate
+        }
     };
     const bool one = m <= kBatch;
     if (one) load(0);
 
-    // ---- the c-th largest key: digit by digit from the top
+    // ---- the c-th largest key.  A row in registers: bit by bit from the top, by
+    // counting the keys not below a candidate; done early when exactly c are.  A
+    // longer row: three digits by histograms, one reading of the row each.
     uint32_t prefix = 0;
     int left = c;  // rank still to find among the keys that share the prefix
-    constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
-#pragma unroll
-    for (int d = 0; d < 3; ++d) {
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = d == 0 ? 0u : 0xffffffffu << (kShift[d] + kBits[d]);
-        for (int base = 0; base < m; base += kBatch) {
-            if (!one) load(base);
+    if (one) {
+        auto at_least = [&](uint32_t cand, int buf) {  // cand > 0: keys past the row are 0
+            int n = 0;
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) {
-                const uint32_t k = key[i];
-                if (base + i * kSelThreads + tid < m && (k & mask) == prefix)
-                    atomicAdd(&hist[(k >> kShift[d]) & ((1u << kBits[d]) - 1)], 1);
+                if (i * kSelThreads >= m) break;
+                n += key[i] >= cand;
             }
+            n = __reduce_add_sync(kFull, n);
+            if (lane == 0) count[buf][warp] = n;
+            __syncthreads();
+            return __reduce_add_sync(kFull, lane < kSelWarps ? count[buf][lane] : 0);
+        };
+        bool exact = false;
+        for (int b = 31; b >= 0 && !exact; --b) {
+            const uint32_t cand = prefix | (1u << b);
+            const int n = at_least(cand, b & 1);
+            if (n >= c) prefix = cand;
+            exact = n == c;
         }
-        __syncthreads();
-        // thread i holds bins kBins-1-2i and kBins-2-2i: counts from the top down
-        const int hi = hist[kBins - 1 - 2 * tid], lo = hist[kBins - 2 - 2 * tid];
-        int incl = hi + lo;
+        if (exact) {
+            prefix -= 1;  // the c keys not below the candidate
+            left = 0;
+        } else {
+            left = c - at_least(prefix + 1, 1);
+        }
+    } else {
+        constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+#pragma unroll 1
+        for (int d = 0; d < 3; ++d) {
+            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+            const uint32_t mask = d == 0 ? 0u : 0xffffffffu << (kShift[d] + kBits[d]);
+            for (int base = 0; base < m; base += kBatch) {
+                load(base);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) wsum[warp] = incl;
-        __syncthreads();
-        if (warp == 0) {
-            const int v = wsum[lane];
-            int x = v;
+                for (int i = 0; i < kKeys; ++i) {
+                    if (base + i * kSelThreads >= m) break;
+                    const uint32_t k = key[i];
+                    if (base + i * kSelThreads + tid < m && (k & mask) == prefix)
+                        atomicAdd(&hist[(k >> kShift[d]) & ((1u << kBits[d]) - 1)], 1);
+                }
+            }
+            __syncthreads();
+            // thread i holds kPerThread bins, counted from the top down
+            constexpr int kPerThread = kBins / kSelThreads;
+            int own = 0;
+#pragma unroll
+            for (int q = 0; q < kPerThread; ++q) own += hist[kBins - 1 - kPerThread * tid - q];
+            int incl = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, x, o);
-                if (lane >= o) x += y;
+                const int y = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += y;
             }
-            wsum[lane] = x - v;
+            if (lane == 31) wsum[warp] = incl;
+            __syncthreads();
+            int before = incl - own;  // keys in higher bins
+            for (int q = 0; q < warp; ++q) before += wsum[q];
+            if (left > before && left <= before + own) {
+                int q = 0;
+                while (true) {
+                    const int n = hist[kBins - 1 - kPerThread * tid - q];
+                    if (left <= before + n) break;
+                    before += n;
+                    ++q;
+                }
+                sh_digit = (uint32_t)(kBins - 1 - kPerThread * tid - q);
+                sh_left = left - before;
+            }
+            __syncthreads();
+            prefix |= sh_digit << kShift[d];
+            left = sh_left;
         }
-        __syncthreads();
-        const int before = wsum[warp] + incl - hi - lo;  // keys in higher bins
-        if (left > before && left <= before + hi + lo) {
-            const bool first = left <= before + hi;
-            sh_digit = (uint32_t)(kBins - 1 - 2 * tid - (first ? 0 : 1));
-            sh_left = left - before - (first ? 0 : hi);
-        }
-        __syncthreads();
-        prefix |= sh_digit << kShift[d];
-        left = sh_left;
     }
     // every key above `prefix` stays, and the first `left` of those equal to it
 
@@ -172,21 +209,26 @@ evict_select_kernel(const EvictParams p) {
         if (!one) load(base);
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            const bool in = base + i * kSelThreads + tid < m;
-            const unsigned bg = __ballot_sync(kFull, in && key[i] > prefix);
-            const unsigned be = __ballot_sync(kFull, in && key[i] == prefix);
+            unsigned bg = 0, be = 0;
+            if (base + i * kSelThreads < m) {
+                const bool in = base + i * kSelThreads + tid < m;
+                bg = __ballot_sync(kFull, in && key[i] > prefix);
+                be = __ballot_sync(kFull, in && key[i] == prefix);
+            }
             if (lane == 0) {
                 run_gt[i * kSelWarps + warp] = __popc(bg);
                 run_eq[i * kSelWarps + warp] = __popc(be);
             }
         }
         __syncthreads();
-        if (warp < 2) {  // exclusive scan of kRuns counts, kKeys per lane; warp 0: gt, warp 1: eq
-            int* run = warp ? run_eq : run_gt;
-            int v[kKeys], sum = 0;
+        if (warp < 2) {  // exclusive scan of kRuns counts, kOwn per lane; warp 0: gt, warp 1: eq
+            constexpr int kOwn = kRuns / 32;
+            static_assert(kOwn * 32 == kRuns, "every run has its lane");
+            int* run = (warp ? run_eq : run_gt) + lane * kOwn;
+            int v[kOwn], sum = 0;
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) {
-                v[i] = run[lane * kKeys + i];
+            for (int i = 0; i < kOwn; ++i) {
+                v[i] = run[i];
                 sum += v[i];
             }
             int x = sum;
@@ -198,14 +240,15 @@ evict_select_kernel(const EvictParams p) {
             if (lane == 31) wsum[warp] = x;
             x -= sum;
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) {
-                run[lane * kKeys + i] = x;
+            for (int i = 0; i < kOwn; ++i) {
+                run[i] = x;
                 x += v[i];
             }
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
+            if (base + i * kSelThreads >= m) break;
             const int t = base + i * kSelThreads + tid;
             const bool is_gt = t < m && key[i] > prefix, is_eq = t < m && key[i] == prefix;
             const unsigned bg = __ballot_sync(kFull, is_gt), be = __ballot_sync(kFull, is_eq);
@@ -220,41 +263,71 @@ evict_select_kernel(const EvictParams p) {
 }
 
 constexpr int kGatThreads = 256;
+constexpr int kGatRows = 2;  // rows a thread has in flight
 
-// CTA: destination block b of sequence s.  Chunk c of row (slot, head): the
-// destination is one contiguous run, the sources rows of the old blocks.
+// CTA: destination block b of sequence s.  kLanes threads hold a row, 16 bytes
+// each; the CTA's rows (slot, head) are walked in the destination's order, which is
+// one contiguous run, so no index needs a division.
+template <int kLanes>
 __global__ void __launch_bounds__(kGatThreads)
-evict_gather_kernel(const EvictParams p, int nblk) {
+evict_gather_kernel(const EvictParams p, int nblk, int lg_bs) {
+    constexpr int kStep = kGatThreads / kLanes;  // rows the CTA copies side by side
+    constexpr int kRowBytes = kLanes * 16;
     const int s = (int)(blockIdx.x / nblk), b = (int)(blockIdx.x % nblk);
     bool bad;
     const int L = evict_len(p, s, &bad);
+    const bool on = L > p.budget;
+    const int dst = on ? __ldg(p.new_tables + (int64_t)s * p.new_mbps + b) : 0;
+    const int c = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
+    int slot = r0 / p.hkv, h = r0 - slot * p.hkv;
+    const int dslot = kStep / p.hkv, dh = kStep - dslot * p.hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (L <= p.budget) return;
-    const int dst = __ldg(p.new_tables + (int64_t)s * p.new_mbps + b);
+    if (!on) return;
     if (dst < 0 || dst >= p.num_blocks) {
         if (threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
         return;
     }
-    const int cpr = p.row_bytes / 16;
     const int slots = min(p.bs, p.budget - b * p.bs);
-    const int chunks = slots * p.hkv * cpr;
     const int32_t* table = p.tables + (int64_t)s * p.mbps;
-    const int64_t dbase = (int64_t)dst * p.bs * p.hkv * p.row_bytes;
-    for (int i = threadIdx.x; i < chunks; i += kGatThreads) {
-        const int row = i / cpr, c = i - row * cpr;
-        const int slot = row / p.hkv, h = row - slot * p.hkv;
-        const int t = p.kept[((int64_t)s * p.hkv + h) * p.budget + b * p.bs + slot];
-        const int src = __ldg(table + t / p.bs);
-        if (src < 0 || src >= p.num_blocks) {
-            if (c == 0) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
-            continue;
+    const int32_t* kept = p.kept + (int64_t)s * p.hkv * p.budget + b * p.bs;
+    int64_t to = ((int64_t)dst * p.bs * p.hkv + r0) * kRowBytes + 16 * c;
+    while (slot < slots) {
+        int t[kGatRows], hh[kGatRows];
+        bool in[kGatRows];
+#pragma unroll
+        for (int i = 0; i < kGatRows; ++i) {
+            in[i] = slot < slots;
+            hh[i] = h;
+            t[i] = in[i] ? kept[(int64_t)h * p.budget + slot] : 0;
+            if ((unsigned)t[i] >= (unsigned)L) { t[i] = 0; in[i] = false; }
+            slot += dslot;
+            h += dh;
+            if (h >= p.hkv) { h -= p.hkv; ++slot; }
         }
-        const int64_t from = (((int64_t)src * p.bs + t % p.bs) * p.hkv + h) * p.row_bytes + 16 * c;
-        const int64_t to = dbase + (int64_t)i * 16;
-        const uint4 k = *reinterpret_cast<const uint4*>(p.kc + from);
-        const uint4 v = *reinterpret_cast<const uint4*>(p.vc + from);
-        *reinterpret_cast<uint4*>(p.kc + to) = k;
-        *reinterpret_cast<uint4*>(p.vc + to) = v;
+        int src[kGatRows];
+#pragma unroll
+        for (int i = 0; i < kGatRows; ++i) src[i] = __ldg(table + (t[i] >> lg_bs));
+        uint4 k[kGatRows], v[kGatRows];
+#pragma unroll
+        for (int i = 0; i < kGatRows; ++i) {
+            if (in[i] && (src[i] < 0 || src[i] >= p.num_blocks)) {
+                if (c == 0) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+                in[i] = false;
+            }
+            if (in[i]) {
+                const int64_t from = ((((int64_t)src[i] << lg_bs) + (t[i] & (p.bs - 1))) * p.hkv + hh[i]) * kRowBytes + 16 * c;
+                k[i] = *reinterpret_cast<const uint4*>(p.kc + from);
+                v[i] = *reinterpret_cast<const uint4*>(p.vc + from);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kGatRows; ++i) {
+            if (in[i]) {
+                *reinterpret_cast<uint4*>(p.kc + to) = k[i];
+                *reinterpret_cast<uint4*>(p.vc + to) = v[i];
+            }
+            to += kStep * kRowBytes;
+        }
     }
 }
 
@@ -279,6 +352,8 @@ extern "C" pkv_status pkv_evict_tokens(void* key_cache, void* value_cache, pkv_d
     if (max_blocks_per_seq <= 0 || (int64_t)max_blocks_per_seq * block_size > 0x7fffffffLL ||
         new_max_blocks_per_seq <= 0 || (int64_t)new_max_blocks_per_seq * block_size > 0x7fffffffLL)
         return fail(PKV_EINVAL, "max_blocks_per_seq out of range");
+    if ((int64_t)max_blocks_per_seq * block_size > 0x40000000LL)  // 32-bit token indexes with room for a batch
+        return fail(PKV_EUNSUPPORTED, "table rows of more than 2^30 tokens");
     if (weight_len <= 0 || new_weight_len <= 0) return fail(PKV_EINVAL, "weight lengths must be positive");
     if (budget <= 0 || recent < 0 || recent > budget) return fail(PKV_EINVAL, "budget > 0 and 0 <= recent <= budget");
     if (num_seqs == 0) return PKV_OK;
@@ -315,7 +390,13 @@ extern "C" pkv_status pkv_evict_tokens(void* key_cache, void* value_cache, pkv_d
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_gather_kernel, p, (int)nblk);
+    const int lg_bs = block_size == 16 ? 4 : 5;
+    switch (p.row_bytes / 16) {
+    case 4: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<4>, p, (int)nblk, lg_bs); break;
+    case 8: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<8>, p, (int)nblk, lg_bs); break;
+    case 16: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<16>, p, (int)nblk, lg_bs); break;
+    default: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<32>, p, (int)nblk, lg_bs); break;
+    }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PKV_ECUDA, "evict gather launch: %s", cudaGetErrorString(e));
     return PKV_OK;
