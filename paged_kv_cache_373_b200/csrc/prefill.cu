@@ -27,14 +27,6 @@
 // with an odd count) splits its tiles instead: group 0 takes the even tiles,
 // group 1 the odd ones, and group 0 merges the two partial (max, sum, O)
 // results at the end.
-// Modified scores (kMod: pkv_paged_prefill_scoremod) change three things: the
-// scores are capped and biased as they leave tensor memory; the mask is
-//   t < prefix  or  (t <= p and t > p - window);
-// and a pair's K/V tiles are those that hold its prefix and then those from its
-// earliest row's window on, the tiles between left out (tile kt of the walk is
-// tile kt of the sequence up to the prefix's last, kt + gap after it).  A block of
-// a walked tile that none of the pair's rows attends is copied from past the
-// pool's end, which TMA fills with zeros: its table entry is not looked at.
 // Every hand-off is an mbarrier; every wait is bounded (0.2 s of
 // %globaltimer): a timeout sets PKV_DEVERR_TIMEOUT, every role leaves its
 // loop, the copies and products already issued are drained, and the CTA
@@ -49,7 +41,7 @@
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
-#include "score_cap.cuh"
+#include "prefill.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -67,7 +59,6 @@ constexpr int kPfStages = 3;        // K and V ring depth
 constexpr int kPfTmemCols = 512;    // unit u: S in columns 256 u + [0, 64), O from 256 u + 64,
 constexpr int kPfTmemP = 192;       //   P (hi, lo: 32 columns each) from 256 (1 - u) + 192: the
                                     //   other half from its O (measured 1 % faster than beside it)
-constexpr uint64_t kPfWaitNs = 200000000ull;
 
 // mbarriers
 enum : int {
@@ -82,28 +73,6 @@ enum : int {
     kBarO = kBarP + 2,                     // [unit] P V finished
     kBarDrain = kBarO + 2,                 // products drained (abort path)
     kNumBars = kBarDrain + 1
-};
-
-struct PrefillParams {
-    void* out;
-    const int32_t* tables;
-    const int32_t* seq_lens;
-    const int32_t* qstart;
-    int* err;
-    int64_t num_blocks;
-    int num_seqs, num_heads, num_kv_heads, g, mbps, bs;
-    float scale_log2;
-    uint64_t wait_ns;  // limit of every wait (kPfWaitNs)
-    int stop_tile;     // < 0; a test of the timeout path sets k >= 0: K/V tiles k, k+1, ... are never copied
-};
-
-// Modified scores (log2 domain; see ModArg in paged_attention.cuh).
-template <bool kMod> struct PfMod {};
-template <> struct PfMod<true> {
-    const float* slopes;         // [num_heads] or null
-    const int32_t* prefix_lens;  // [num_seqs] or null
-    float cap2, pre;             // pre = scale_log2 / cap2; cap2 = 0: no cap
-    int window;                  // 0: no window
 };
 
 // Named barrier over one softmax group (kPfGroup threads, whole warps) that
@@ -138,11 +107,10 @@ struct PfUnit {
     int tok0, ntok, pos0, kv_end, nkv;
 };
 
-template <typename T, int D, bool kMod>
+template <typename T, int D>
 __global__ void __launch_bounds__(kPfThreads, 1)
 pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmap_q,
-                   const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                   const PfMod<kMod> md) {
+                   const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
     using SM = PfSmem<T, D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr int CH = D / 8;  // 16-byte chunks per row
@@ -212,34 +180,17 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
     const int tpu = kPfRows / p.g;  // chunk tokens per unit (g divides 16)
     const int j0 = nrt_s - 1 - 2 * jp, j1 = j0 - 1;
     const int nunits = j1 >= 0 ? 2 : 1;
-    int pre = 0, window = 0;  // visible: t < pre or (t <= pos and t > pos - window)
-    if constexpr (kMod) {
-        if (md.prefix_lens) pre = min(max(__ldg(md.prefix_lens + s), 0), L);
-        window = md.window;
-    }
     auto make_unit = [&](int j) {
         PfUnit w;
         w.tok0 = j * tpu;
         w.ntok = min(tpu, C - w.tok0);
         w.pos0 = ctx + w.tok0;
         w.kv_end = w.pos0 + w.ntok;
-        if constexpr (kMod) w.kv_end = max(w.kv_end, pre);
         w.nkv = (w.kv_end + kPfTok - 1) / kPfTok;
         return w;
     };
-    PfUnit U0 = make_unit(j0);                 // the later rows: the longer K/V range
-    PfUnit U1 = make_unit(j1 >= 0 ? j1 : j0);  // (the same when nunits == 1)
-    // the walk's tiles: those of the prefix, then those from the earliest row's
-    // window on.  Every unit has a row whose window starts at or after `first`
-    // and ends before kv_end, so it keeps a tile past the gap.
-    int first = 0, gap = 0;
-    if constexpr (kMod) {
-        first = window > 0 ? max(U1.pos0 - window + 1, 0) : 0;
-        gap = max(first / kPfTok - (pre + kPfTok - 1) / kPfTok, 0);
-        U0.nkv -= gap;
-        U1.nkv -= gap;
-    }
-    auto tile_token = [&](int kt) { return (!kMod || kt * kPfTok < pre ? kt : kt + gap) * kPfTok; };
+    const PfUnit U0 = make_unit(j0);                 // the later rows: the longer K/V range
+    const PfUnit U1 = make_unit(j1 >= 0 ? j1 : j0);  // (unused when nunits == 1)
     const int nkv = U0.nkv;
     // a unit alone splits its K/V tiles between the two groups (even / odd
     // tiles), whose partial results are merged at the end
@@ -276,10 +227,7 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
             const uint32_t tS = tmem + lane_addr + X * 256 + half * (kPfTok / 2);
             const uint32_t tO = tmem + lane_addr + X * 256 + kPfTok + half * (D / 2);
             const uint32_t tP = tmem + lane_addr + (X ^ 1) * 256 + kPfTmemP + half * (kPfTok / 4);
-            const float sl2 = kMod ? 1.f : p.scale_log2;  // modified scores leave the cap in the log2 domain
-            float slope2 = 0.f;
-            if constexpr (kMod)
-                if (md.slopes) slope2 = __ldg(md.slopes + (int64_t)kh * p.g + row % p.g) * 1.4426950408889634f;
+            const float sl2 = p.scale_log2;
             float mref = -INFINITY, l = 0.f;  // reference maximum (log2 domain) and this half's sum
             bool failed = false;
 #pragma unroll 1
@@ -292,32 +240,8 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
                 if (ok) {
                     tc_after_sync();
                     tc_ld32(tS, sc);
-                    const int tt = tile_token(kt);
-                    if constexpr (kMod) {
-                        const int t0 = tt + half * (kPfTok / 2);
-                        if (md.cap2 > 0.f) {
-                            cap_scores(sc, md.pre, md.cap2);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < kPfTok / 2; ++c) sc[c] *= p.scale_log2;
-                        }
-                        if (md.slopes) {
-                            const float d0 = (float)(pos - t0);
-#pragma unroll
-                            for (int c = 0; c < kPfTok / 2; ++c) sc[c] = fmaf(-slope2, fabsf(d0 - (float)c), sc[c]);
-                        }
-                        // tiles with a token past the first row, or at or before the last row's window
-                        const int last = U.pos0 + U.ntok - 1;
-                        if (tt + kPfTok - 1 > U.pos0 || (window > 0 && tt <= last - window)) {
-                            const int lo = window > 0 ? pos - window : -1;
-#pragma unroll
-                            for (int c = 0; c < kPfTok / 2; ++c) {
-                                const int t = t0 + c;
-                                sc[c] = t < pre || (t <= pos && t > lo) ? sc[c] : -INFINITY;
-                            }
-                        }
-                    } else if (tt + kPfTok - 1 > U.pos0) {  // a tile on the causal diagonal
-                        const int t0 = tt + half * (kPfTok / 2);
+                    if (kt * kPfTok + kPfTok - 1 > U.pos0) {  // a tile on the causal diagonal
+                        const int t0 = kt * kPfTok + half * (kPfTok / 2);
 #pragma unroll
                         for (int c = 0; c < kPfTok / 2; ++c) sc[c] = t0 + c <= pos ? sc[c] : -INFINITY;
                     }
@@ -578,14 +502,9 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
                 int nb = 0;
 #pragma unroll
                 for (int jb = 0; jb < kPfTok / 16; ++jb) {
-                    const int t = tile_token(kt) + (jb << lg_bs);
+                    const int t = kt * kPfTok + (jb << lg_bs);
                     phys[jb] = 0;
                     if (jb < nblk && t < U0.kv_end) {
-                        if (kMod && t >= pre && t + p.bs <= first) {
-                            phys[jb] = (int)p.num_blocks;  // no row attends it: zeros from past the pool
-                            ++nb;
-                            continue;
-                        }
                         int ph = __ldg(trow + (t >> lg_bs));
                         if (ph < 0 || ph >= p.num_blocks) {
                             raise_error(p.err, PKV_DEVERR_BLOCK_ID);
@@ -631,7 +550,7 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
             bool fine = ok && mbar_wait(bar(kBarVFull + st), pass(kl), abort, p.wait_ns);
             fine = __all_sync(kFull, fine);
             if (fine) {
-                const int r0 = U0.kv_end - tile_token(kl);
+                const int r0 = U0.kv_end - kl * kPfTok;
                 uint8_t* vt = vsm + st * SM::kTile;
                 for (int i = lane; i < (kPfTok - r0) * CH; i += 32)
                     *reinterpret_cast<uint4*>(vt + tc_off(r0 + i / CH, i % CH, kPfTok)) = make_uint4(0, 0, 0, 0);
@@ -651,9 +570,9 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
     if (tid == 0 && abort_flag) raise_error(p.err, PKV_DEVERR_TIMEOUT);
 }
 
-template <typename T, int D, bool kMod>
-pkv_status launch_prefill(const PrefillParams& p, const PfMod<kMod>& md, const void* query, const void* kc,
-                          const void* vc, int64_t num_tokens, int64_t num_blocks, int64_t grid, cudaStream_t st) {
+template <typename T, int D>
+pkv_status launch_prefill(const PrefillParams& p, const void* query, const void* kc, const void* vc,
+                          int64_t num_tokens, int64_t num_blocks, int64_t grid, cudaStream_t st) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr int kSmem = PfSmem<T, D>::kBytes;
     static_assert(kSmem <= 227 * 1024 - 8 * 1024, "prefill shared memory");
@@ -667,30 +586,30 @@ pkv_status launch_prefill(const PrefillParams& p, const PfMod<kMod>& md, const v
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(PKV_ECUDA, "cudaGetDevice");
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(pkv_prefill_kernel<T, D, kMod>,
+        const cudaError_t e = cudaFuncSetAttribute(pkv_prefill_kernel<T, D>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return fail(PKV_ECUDA, "prefill smem opt-in: %s", cudaGetErrorString(e));
         configured.fetch_or(bit);
     }
-    pkv_prefill_kernel<T, D, kMod><<<(unsigned)grid, kPfThreads, kSmem, st>>>(p, tq, tk, tv, md);
+    pkv_prefill_kernel<T, D><<<(unsigned)grid, kPfThreads, kSmem, st>>>(p, tq, tk, tv);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PKV_ECUDA, "prefill launch: %s", cudaGetErrorString(e));
     return PKV_OK;
 }
 
-// A timeout test armed by pkv_testing_prefill_timeout for the next
-// pkv_paged_prefill call on this thread (stop_tile < 0: not armed).
+// A timeout test armed by pkv_testing_prefill_timeout for the next prefill call
+// on this thread (stop_tile < 0: not armed).
 thread_local int t_test_stop_tile = -1;
 thread_local uint64_t t_test_wait_ns = 0;
 
-// Validate the arguments of a prefill call, then launch it with plain or
-// modified scores.
-template <bool kMod>
-pkv_status prefill(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache, const void* value_cache,
-                   pkv_dtype cache_dtype, const int32_t* block_tables, int max_blocks_per_seq,
-                   const int32_t* seq_lens, const int32_t* query_start, int num_seqs, int64_t num_query_tokens,
-                   int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
-                   PfMod<kMod> md, pkv_stream_t stream) {
+}  // namespace
+
+pkv_status prefill_prepare(PrefillParams* pp, int64_t* grid_out, void* out, const void* query, pkv_dtype q_dtype,
+                           const void* key_cache, const void* value_cache, pkv_dtype cache_dtype,
+                           const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                           const int32_t* query_start, int num_seqs, int64_t num_query_tokens, int num_heads,
+                           int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale) {
+    *grid_out = 0;
     // a timeout test applies to this call only, whatever it returns
     const int stop_tile = t_test_stop_tile;
     const uint64_t wait_ns = t_test_wait_ns ? t_test_wait_ns : kPfWaitNs;
@@ -730,10 +649,6 @@ pkv_status prefill(void* out, const void* query, pkv_dtype q_dtype, const void* 
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_ns = wait_ns;
     p.stop_tile = stop_tile;
-    if constexpr (kMod) {
-        md.pre *= p.scale_log2;
-        if (!(md.pre < INFINITY)) return fail(PKV_EINVAL, "scale / softcap overflows fp32");
-    }
     // unit pairs: sum_s ceil(ceil(C_s g / 128) / 2) <= ceil(T g / 256) + S
     const int64_t pairs = (num_query_tokens * g + 2 * kPfRows - 1) / (2 * kPfRows) + num_seqs;
     const int64_t grid = pairs * num_kv_heads;
@@ -741,18 +656,11 @@ pkv_status prefill(void* out, const void* query, pkv_dtype q_dtype, const void* 
     // TMA coordinates are 32-bit: token rows of the query and of the pool
     if (num_query_tokens > 0x7fffffffLL || num_blocks * block_size > 0x7fffffffLL)
         return fail(PKV_EUNSUPPORTED, "query or pool too large for 32-bit copy coordinates");
-    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t T = num_query_tokens;
-    if (cache_dtype == PKV_F16)
-        return head_dim == 64
-                   ? launch_prefill<__half, 64, kMod>(p, md, query, key_cache, value_cache, T, num_blocks, grid, cs)
-                   : launch_prefill<__half, 128, kMod>(p, md, query, key_cache, value_cache, T, num_blocks, grid, cs);
-    return head_dim == 64
-               ? launch_prefill<__nv_bfloat16, 64, kMod>(p, md, query, key_cache, value_cache, T, num_blocks, grid, cs)
-               : launch_prefill<__nv_bfloat16, 128, kMod>(p, md, query, key_cache, value_cache, T, num_blocks, grid, cs);
+    *pp = p;
+    *grid_out = grid;
+    return PKV_OK;
 }
 
-}  // namespace
 }  // namespace pkv
 
 using namespace pkv;
@@ -774,22 +682,20 @@ extern "C" pkv_status pkv_paged_prefill(void* out, const void* query, pkv_dtype 
                                         int64_t num_query_tokens, int num_heads, int num_kv_heads,
                                         int head_dim, int block_size, int64_t num_blocks, float scale,
                                         pkv_stream_t stream) {
-    return prefill(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, max_blocks_per_seq, seq_lens,
-                   query_start, num_seqs, num_query_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
-                   scale, PfMod<false>{}, stream);
-}
-
-extern "C" pkv_status pkv_paged_prefill_scoremod(
-    void* out, const void* query, pkv_dtype q_dtype, const void* key_cache, const void* value_cache,
-    pkv_dtype cache_dtype, const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
-    const int32_t* query_start, int num_seqs, int64_t num_query_tokens, int num_heads, int num_kv_heads,
-    int head_dim, int block_size, int64_t num_blocks, float scale, float softcap, int window,
-    const float* alibi_slopes, const int32_t* prefix_lens, pkv_stream_t stream) {
-    PfMod<true> md{alibi_slopes, prefix_lens, 0.f, 0.f, window};
-    const pkv_status st = score_cap(softcap, &md.cap2, &md.pre);
-    if (st != PKV_OK) return st;
-    if (window < 0) return fail(PKV_EINVAL, "window < 0");
-    return prefill(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, max_blocks_per_seq, seq_lens,
-                   query_start, num_seqs, num_query_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
-                   scale, md, stream);
+    PrefillParams p;
+    int64_t grid = 0;
+    const pkv_status st = prefill_prepare(&p, &grid, out, query, q_dtype, key_cache, value_cache, cache_dtype,
+                                          block_tables, max_blocks_per_seq, seq_lens, query_start, num_seqs,
+                                          num_query_tokens, num_heads, num_kv_heads, head_dim, block_size,
+                                          num_blocks, scale);
+    if (st != PKV_OK || grid == 0) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t T = num_query_tokens;
+    if (cache_dtype == PKV_F16)
+        return head_dim == 64
+                   ? launch_prefill<__half, 64>(p, query, key_cache, value_cache, T, num_blocks, grid, cs)
+                   : launch_prefill<__half, 128>(p, query, key_cache, value_cache, T, num_blocks, grid, cs);
+    return head_dim == 64
+               ? launch_prefill<__nv_bfloat16, 64>(p, query, key_cache, value_cache, T, num_blocks, grid, cs)
+               : launch_prefill<__nv_bfloat16, 128>(p, query, key_cache, value_cache, T, num_blocks, grid, cs);
 }

@@ -1,0 +1,618 @@
+// prefill_scoremod.cu -- pkv_paged_prefill_scoremod: chunked-prefill attention
+// over the paged cache with modified scores.  A row at position p attends
+//   t < prefix  or  (t <= p and t > p - window),
+// with scores x = scale q.k, capped (cap tanh(x / cap)) and biased
+// (- slope |p - t|).
+//
+// Unit: (sequence, kv head, 128 query rows), a row being a (chunk token, q head
+// of the kv head's group) pair; a CTA takes two adjacent units of one (sequence,
+// kv head), which read the same K/V tiles of 128 tokens, and keeps the tensor
+// core on one unit while the other runs its softmax:
+//   - warps 0-3 and 4-7: the units' softmax, one thread per row, so that a row's
+//     maximum and sum need no exchange: all 128 scores of a tile come from tensor
+//     memory in one load, are capped, biased and masked in registers (by pairs,
+//     fp32x2), exponentiated against a reference maximum, and P goes back over the
+//     scores (bf16 as hi + lo parts: 64 + 64 columns, exactly the 128 of S), where
+//     the P V product reads it as its A operand.  O stays in tensor memory and is
+//     rescaled only when a row's maximum passes its reference by 2^8;
+//   - warp 8 (one lane) owns tensor memory (S_0, S_1, O_0, O_1: 512 columns) and
+//     issues, per tile, O_0 += P_0 V, S_0' = Q_0 K'^T, O_1 += P_1 V, S_1' = Q_1 K'^T.
+//     Products issued by one thread run in order, so S' may overwrite the P that the
+//     product before it reads, and a finished S' says that O is settled;
+//   - warps 9 and 10 copy the K and the V tiles (2-stage rings) with TMA through the
+//     block table, a lane per box.
+// A pair's tiles are those that hold its prefix and then those from its earliest
+// row's window on; the tiles between (tile kt of the walk is tile kt of the sequence
+// up to the prefix's last, kt + gap after it) are left out.  A block of a walked tile
+// that none of the pair's rows attends is copied from past the pool's end, which TMA
+// fills with zeros: its table entry is not looked at.
+// A unit without a partner splits its tiles instead: group 0 takes the even tiles,
+// group 1 the odd ones, and group 0 merges the two partial results at the end.
+// Every hand-off is an mbarrier and every wait is bounded, as in prefill.cu.
+//
+// Bound: the tensor core by its products (with P in two parts 1.5 times the
+// algorithm's), then the softmax warps' issue slots.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <cmath>
+#include <type_traits>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "prefill.cuh"
+#include "score_cap.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;          // query rows per unit (tensor-core M)
+constexpr int kTok = 128;           // KV tokens per tile (N of S, K of P V)
+constexpr int kStages = 2;          // K and V ring depth
+constexpr int kSoftWarps = 8;       // 4 per unit: a thread per row
+constexpr int kMmaWarp = 8, kLoadK = 9, kLoadV = 10;
+constexpr int kThreads = 12 * 32;   // (warp 11 only fills the last register group)
+// Registers per thread: the launch's 168 (12 warps of 168 are what an SM has),
+// shifted from the issuing warps to the softmax warps, which hold a whole row of
+// scores: 2 * 128 * 224 + 128 * 56 = 384 * 168.
+constexpr int kRegsSoft = 224, kRegsIssue = 56, kRegsLaunch = 168;
+static_assert(kSoftWarps * kRegsSoft + (kThreads / 32 - kSoftWarps) * kRegsIssue == kThreads / 32 * kRegsLaunch,
+              "the shares add up to the launch's registers");
+constexpr int kTmemCols = 512;      // S_X in columns 128 X.., O_X from 256 + 128 X
+
+enum : int {
+    kBarQ = 0,                         // q rows landed
+    kBarKFull = 1,                     // [stage] K tile landed
+    kBarVFull = kBarKFull + kStages,   // [stage] V tile landed
+    kBarKEmpty = kBarVFull + kStages,  // [stage] every S product of the K stage finished
+    kBarVEmpty = kBarKEmpty + kStages, // [stage] every P V product of the V stage finished
+    kBarVFix = kBarVEmpty + kStages,   // the last V tile's rows past the unit's end are zeroed
+    kBarS = kBarVFix + 1,              // [unit] S ready (and O settled)
+    kBarP = kBarS + 2,                 // [unit] P written: kRows arrivals
+    kBarO = kBarP + 2,                 // [unit] the last P V finished
+    kBarDrain = kBarO + 2,             // products drained
+    kNumBars = kBarDrain + 1
+};
+
+struct PfMod {
+    const float* slopes;         // [num_heads] or null
+    const int32_t* prefix_lens;  // [num_seqs] or null
+    float cap2, pre;             // cap log2(e) (0: no cap), scale / cap
+    int window;                  // 0: no window
+};
+
+struct Unit {
+    int tok0, ntok, pos0, kv_end, nkv;
+};
+
+template <typename T, int D>
+struct Smem {
+    static constexpr int kQ = kRows * D * 2;     // one unit's q rows
+    static constexpr int kTile = kTok * D * 2;   // one K or V tile
+    static constexpr int kParts = std::is_same<T, __nv_bfloat16>::value ? 2 : 1;  // P hi (+ lo)
+    static constexpr int kData = 2 * kQ + 2 * kStages * kTile + 1024;             // + alignment
+    // at least 120 KB, so one CTA (and its 512 tensor-memory columns) per SM
+    static constexpr int kBytes = kData > 120 * 1024 ? kData : 120 * 1024;
+};
+
+// Barrier over both softmax groups that also ORs a flag across them.
+__device__ __forceinline__ bool soft_sync_or(bool flag) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}\n"
+                 : "=r"(r) : "r"((uint32_t)flag), "n"(kSoftWarps * 32) : "memory");
+    return r != 0;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmap_q,
+                            const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                            const PfMod md) {
+    using SM = Smem<T, D>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int CB = D / 64;  // 128-byte column blocks per row
+    extern __shared__ uint8_t pf_raw[];
+    uint8_t* sm = pf_raw + ((1024 - (smem_u32(pf_raw) & 1023)) & 1023);  // 1024-byte aligned operands
+    uint8_t* qsm = sm;                        // [2 units]
+    uint8_t* ksm = qsm + 2 * SM::kQ;          // [stage]
+    uint8_t* vsm = ksm + kStages * SM::kTile; // [stage]
+    __shared__ __align__(8) uint64_t bars[kNumBars];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    __shared__ float xsum[kRows], xref[kRows];  // group 1's row sums and references (split unit)
+    volatile int* abort = &abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto stg = [](int kt) { return kt % kStages; };
+    auto pass = [](int kt) { return (uint32_t)((kt / kStages) & 1); };
+
+    // ---- the unit pair: kv head from the block index, then pair u among all
+    // sequences' pairs (a warp-parallel scan that every warp does).  A
+    // sequence's row tiles pair from the last: (n-1, n-2), (n-3, n-4), ...
+    const int kh = (int)(blockIdx.x % p.num_kv_heads);
+    const int64_t u = blockIdx.x / p.num_kv_heads;
+    int s = -1, jp = 0, nrt_s = 0;
+    {
+        int64_t base = 0;
+        for (int s0 = 0; s0 < p.num_seqs && s < 0; s0 += 32) {
+            const int si = s0 + lane;
+            int nrt = 0;
+            if (si < p.num_seqs) {
+                const int C = __ldg(p.qstart + si + 1) - __ldg(p.qstart + si);
+                if (C < 0 && blockIdx.x == 0 && warp == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
+                nrt = C > 0 ? (int)(((int64_t)C * p.g + kRows - 1) / kRows) : 0;
+            }
+            const int npr = (nrt + 1) >> 1;
+            int incl = npr;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const int64_t lo = base + incl - npr;
+            const unsigned hit = __ballot_sync(kFull, npr > 0 && u >= lo && u < lo + npr);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                s = s0 + src;
+                const int64_t l0 = __shfl_sync(kFull, lo, src);
+                nrt_s = __shfl_sync(kFull, nrt, src);
+                jp = (int)(u - l0);  // a sequence's heaviest pair first
+            }
+            base += __shfl_sync(kFull, incl, 31);
+        }
+    }
+    if (s < 0) return;  // past the last pair
+    const int q0 = __ldg(p.qstart + s);
+    const int C = __ldg(p.qstart + s + 1) - q0;
+    const int L = __ldg(p.seq_lens + s);
+    if (L < C || L > p.mbps * p.bs) {
+        if (tid == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
+        return;
+    }
+    const int pre = md.prefix_lens ? min(max(__ldg(md.prefix_lens + s), 0), L) : 0;
+    const int window = md.window;
+    const int tpu = kRows / p.g;  // chunk tokens per unit (g divides 16)
+    const int j0 = nrt_s - 1 - 2 * jp, j1 = j0 - 1;
+    const int nunits = j1 >= 0 ? 2 : 1;
+    auto make_unit = [&](int j) {
+        Unit w;
+        w.tok0 = j * tpu;
+        w.ntok = min(tpu, C - w.tok0);
+        w.pos0 = L - C + w.tok0;
+        w.kv_end = max(w.pos0 + w.ntok, pre);
+        w.nkv = (w.kv_end + kTok - 1) / kTok;
+        return w;
+    };
+    Unit U0 = make_unit(j0);                 // the later rows: the longer K/V range
+    Unit U1 = make_unit(j1 >= 0 ? j1 : j0);  // (the same when nunits == 1)
+    // the walk's tiles: those of the prefix, then those from the earliest row's
+    // window on.  Every unit has a row whose window starts at or after `first`
+    // and ends before kv_end, so it keeps a tile past the gap.
+    const int first = window > 0 ? max(U1.pos0 - window + 1, 0) : 0;
+    const int gap = max(first / kTok - (pre + kTok - 1) / kTok, 0);
+    U0.nkv -= gap;
+    U1.nkv -= gap;
+    auto tile_token = [&](int kt) { return (kt * kTok < pre ? kt : kt + gap) * kTok; };
+    const int nkv = U0.nkv;
+    // a unit alone splits its K/V tiles between the two groups (even / odd
+    // tiles), whose partial results are merged at the end
+    const bool split = nunits == 1;
+    const bool need_fix = (U0.kv_end % kTok) != 0;  // V rows past the end must read as zeros
+
+    // ---- tensor memory, barriers
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i == kBarP || i == kBarP + 1) ? kRows : 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        abort_flag = 0;
+    }
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = tmem_base;
+
+    if (warp < kSoftWarps) {
+        // ================= softmax group X: unit X (or, for a unit alone, its
+        // tiles of parity X), a thread per row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        const int X = warp >> 2;
+        const Unit U = X && !split ? U1 : U0;
+        const int kt0 = split ? X : 0, kstep = split ? 2 : 1;  // this group's tiles
+        const int ntiles = split ? (nkv - X + 1) / 2 : U.nkv;
+        const int row = (warp & 3) * 32 + lane;
+        const int pos = (row / p.g < U.ntok) ? U.pos0 + row / p.g : -1;
+        const int last = U.pos0 + U.ntok - 1;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_addr + X * kTok;
+        const uint32_t tO = tmem + lane_addr + 256 + X * 128;
+        const bool capped = md.cap2 > 0.f, biased = md.slopes != nullptr;
+        // scores leave the cap as tanh values; without a bias their last factor
+        // is applied in the exponent
+        const float mult = capped ? md.cap2 : p.scale_log2;
+        const float emul = biased ? 1.f : mult;
+        const float slope2 = biased ? __ldg(md.slopes + (int64_t)kh * p.g + row % p.g) * 1.4426950408889634f : 0.f;
+        float mref = -INFINITY, l = 0.f;  // reference maximum (log2 domain) and sum of the row
+        bool failed = false;
+#pragma unroll 1
+        for (int i = 0; i < ntiles; ++i) {
+            const int tt = tile_token(kt0 + i * kstep);
+            bool ok = mbar_wait(bar(kBarS + X), i & 1, abort, p.wait_ns);
+            ok = __all_sync(kFull, ok);
+            if (!ok) {
+                failed = true;
+                break;
+            }
+            tc_after_sync();
+            float sc[kTok];
+            tc_ld128(tS, sc);
+            if (capped) cap_pairs(sc, md.pre);
+            if (biased) {
+                const float d0 = (float)(pos - tt);
+#pragma unroll
+                for (int c = 0; c < kTok; ++c) sc[c] = fmaf(sc[c], mult, -slope2 * fabsf(d0 - (float)c));
+            }
+            // tiles with a token past the first row, or at or before the last row's window
+            if (tt + kTok - 1 > U.pos0 || (window > 0 && tt <= last - window)) {
+                // columns attended: below `pc`, or in [lo, hi]
+                const int pc = pre - tt, hi = pos - tt, lo = window > 0 ? pos - window + 1 - tt : -tt;
+#pragma unroll
+                for (int c = 0; c < kTok; ++c) sc[c] = c < pc || (c <= hi && c >= lo) ? sc[c] : -INFINITY;
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kTok; c += 2) m4[(c >> 1) & 3] = fmaxf(m4[(c >> 1) & 3], fmaxf(sc[c], sc[c + 1]));
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * emul;
+            const bool grow = mx > mref + 8.f;  // also the first finite maximum
+            float alpha = 1.f;
+            if (grow) {
+                alpha = ex2(mref - mx);  // 0 while nothing was attended
+                l *= alpha;
+                mref = mx;
+            }
+            if (i > 0 && __any_sync(kFull, grow)) {  // rescale O (settled: S of this tile was issued after it)
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                    float v[16];
+                    tc_ld16(tO + c0, v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] *= alpha;
+                    tc_st16(tO + c0, v);
+                }
+            }
+            const float ref = mref == -INFINITY ? 0.f : mref;
+            const F2 em2 = f2(emul, emul), nref2 = f2(-ref, -ref), minus1 = f2(-1.f, -1.f);
+            F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+            for (int c0 = 0; c0 < kTok; c0 += 32) {  // P over the scores, two tokens per 32-bit column
+                uint32_t h[16], lo[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 x = f2_get(f2_fma(f2(sc[c0 + 2 * e], sc[c0 + 2 * e + 1]), em2, nref2));
+                    const float a = ex2(x.x), b = ex2(x.y);
+                    const F2 ab = f2(a, b);
+                    sum[e & 1] = f2_add(sum[e & 1], ab);
+                    h[e] = pack2<kBf16>(a, b);
+                    if constexpr (kBf16) {
+                        const float2 hf = unpack2<true>(h[e]);
+                        const float2 r = f2_get(f2_fma(f2(hf.x, hf.y), minus1, ab));
+                        lo[e] = pack2<true>(r.x, r.y);
+                    }
+                }
+                tc_st16u(tS + c0 / 2, h);
+                if constexpr (kBf16) tc_st16u(tS + kTok / 2 + c0 / 2, lo);
+            }
+            const float2 s2 = f2_get(f2_add(sum[0], sum[1]));
+            l += s2.x + s2.y;
+            tc_wait_st();
+            tc_before_sync();
+            mbar_arrive(bar(kBarP + X));
+        }
+        // ---- the last P V, then normalise (a split unit also merges group 1's
+        // partial result) and store
+        bool ok = !failed && (ntiles == 0 || mbar_wait(bar(kBarO + X), 0, abort, p.wait_ns));
+        if (split && X == 0 && nkv > 1) ok = ok && mbar_wait(bar(kBarO + 1), 0, abort, p.wait_ns);  // read in the merge
+        ok = __all_sync(kFull, ok);
+        bool merge = false;
+        if (split) {
+            if (X == 1) {
+                xsum[row] = l;
+                xref[row] = mref;
+            }
+            ok = !soft_sync_or(!ok);
+            merge = nkv > 1;
+        }
+        if (ok && !(split && X == 1)) {
+            tc_after_sync();
+            float lt = l, a0 = 1.f, a1 = 0.f;
+            if (merge) {
+                const float m1 = xref[row], m = fmaxf(mref, m1);
+                a0 = mref == -INFINITY ? 0.f : ex2(mref - m);
+                a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                lt = a0 * lt + a1 * xsum[row];
+            }
+            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            a0 *= inv;
+            a1 *= inv;
+            T* out = static_cast<T*>(p.out) +
+                     ((int64_t)(q0 + U.tok0 + row / p.g) * p.num_heads + (int64_t)kh * p.g + row % p.g) * D;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+                float v[16];
+                tc_ld16(tO + c0, v);  // every lane loads (warp-collective); only real rows store
+                if (merge) {
+                    float v1[16];
+                    tc_ld16(tO + 128 + c0, v1);  // group 1's O
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = a0 * v[e] + a1 * v1[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] *= a0;
+                }
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = pack2<kBf16>(v[2 * e], v[2 * e + 1]);
+                if (pos >= 0) {
+                    *reinterpret_cast<uint4*>(out + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(out + c0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+        }
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kMmaWarp) {
+        // ================= tensor-core issue (one lane)
+        if (lane == 0) {
+            const uint32_t id_s = tc_idesc<kBf16>(kRows, kTok, 0);
+            const uint32_t id_o = tc_idesc<kBf16>(kRows, D, 1);
+            const uint64_t dq0 = tc_desc(smem_u32(qsm), 16, 1024);
+            const uint64_t dq1 = tc_desc(smem_u32(qsm + (split ? 0 : SM::kQ)), 16, 1024);
+            const uint64_t dk0 = tc_desc(smem_u32(ksm), 16, 1024);
+            const uint64_t dv0 = tc_desc(smem_u32(vsm), kTok * 128, 1024);
+            auto issue_s = [&](int X, int st) {  // S_X = Q_X K^T (a split unit: both groups read q slot 0)
+                const uint64_t qd = X ? dq1 : dq0;
+                const uint64_t kd = desc_add(dk0, (uint32_t)(st * (SM::kTile >> 4)));
+                const uint32_t d = tmem + X * kTok;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma(d, desc_add(qd, ((kk >> 2) * kRows * 128 + (kk & 3) * 32) >> 4),
+                           desc_add(kd, ((kk >> 2) * kTok * 128 + (kk & 3) * 32) >> 4), id_s, kk > 0);
+                tc_commit(bar(kBarS + X));
+            };
+            auto issue_pv = [&](int X, int st, bool acc) {  // O_X (+)= P_X V (hi, then lo; P over S_X)
+                const uint64_t vd = desc_add(dv0, (uint32_t)(st * (SM::kTile >> 4)));
+                const uint32_t d = tmem + 256 + X * 128, a = tmem + X * kTok;
+#pragma unroll
+                for (int part = 0; part < SM::kParts; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kTok / 16; ++kk)
+                        tc_mma_ts(d, a + part * (kTok / 2) + kk * 8, desc_add(vd, (kk * 2048) >> 4), id_o,
+                                  (acc || part > 0 || kk > 0) ? 1u : 0u);
+            };
+            bool ok = mbar_wait(bar(kBarQ), 0, abort, p.wait_ns);
+            if (!split) {
+                ok = ok && mbar_wait(bar(kBarKFull), 0, abort, p.wait_ns);
+                if (ok) {
+                    tc_after_sync();
+                    issue_s(0, 0);
+                    issue_s(1, 0);
+                    tc_commit(bar(kBarKEmpty));
+                }
+#pragma unroll 1
+                for (int kt = 0; ok && kt < nkv; ++kt) {
+                    const int st = stg(kt), sn = stg(kt + 1);
+                    const bool a1 = kt < U1.nkv, a1n = kt + 1 < U1.nkv;
+                    ok = mbar_wait(bar(kBarVFull + st), pass(kt), abort, p.wait_ns) &&
+                         (kt != nkv - 1 || !need_fix || mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) &&
+                         mbar_wait(bar(kBarP), kt & 1, abort, p.wait_ns);
+                    if (!ok) break;
+                    tc_after_sync();
+                    issue_pv(0, st, kt > 0);
+                    if (kt == nkv - 1) tc_commit(bar(kBarO));
+                    if (!a1) tc_commit(bar(kBarVEmpty + st));
+                    if (kt + 1 < nkv) {
+                        ok = mbar_wait(bar(kBarKFull + sn), pass(kt + 1), abort, p.wait_ns);
+                        if (!ok) break;
+                        tc_after_sync();
+                        issue_s(0, sn);
+                        if (!a1n) tc_commit(bar(kBarKEmpty + sn));
+                    }
+                    if (a1) {
+                        ok = mbar_wait(bar(kBarP + 1), kt & 1, abort, p.wait_ns);
+                        if (!ok) break;
+                        tc_after_sync();
+                        issue_pv(1, st, kt > 0);
+                        if (!a1n) tc_commit(bar(kBarO + 1));
+                        tc_commit(bar(kBarVEmpty + st));
+                        if (a1n) {
+                            issue_s(1, sn);
+                            tc_commit(bar(kBarKEmpty + sn));
+                        }
+                    }
+                }
+            } else {
+                // a split unit: group X takes tiles 2 i + X
+#pragma unroll 1
+                for (int kt = 0; ok && kt < 2 && kt < nkv; ++kt) {
+                    ok = mbar_wait(bar(kBarKFull + stg(kt)), pass(kt), abort, p.wait_ns);
+                    if (!ok) break;
+                    tc_after_sync();
+                    issue_s(kt, stg(kt));
+                    tc_commit(bar(kBarKEmpty + stg(kt)));
+                }
+#pragma unroll 1
+                for (int kt = 0; ok && kt < nkv; ++kt) {
+                    const int X = kt & 1;
+                    ok = mbar_wait(bar(kBarVFull + stg(kt)), pass(kt), abort, p.wait_ns) &&
+                         (kt != nkv - 1 || !need_fix || mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) &&
+                         mbar_wait(bar(kBarP + X), (kt >> 1) & 1, abort, p.wait_ns);
+                    if (!ok) break;
+                    tc_after_sync();
+                    issue_pv(X, stg(kt), kt > 1);
+                    if (kt + 2 >= nkv) tc_commit(bar(kBarO + X));
+                    tc_commit(bar(kBarVEmpty + stg(kt)));
+                    if (kt + 2 < nkv) {
+                        ok = mbar_wait(bar(kBarKFull + stg(kt + 2)), pass(kt + 2), abort, p.wait_ns);
+                        if (!ok) break;
+                        tc_after_sync();
+                        issue_s(X, stg(kt + 2));
+                        tc_commit(bar(kBarKEmpty + stg(kt + 2)));
+                    }
+                }
+            }
+            tc_commit(bar(kBarDrain));  // every product issued has finished before tensor memory is freed
+            mbar_wait(bar(kBarDrain), 0, nullptr, p.wait_ns);
+        }
+        __syncwarp();
+    } else if (warp <= kLoadV) {
+        // ================= TMA copies: warp kLoadK the q rows and the K tiles,
+        // warp kLoadV the V tiles; a lane per 64-element box
+        const bool is_k = warp == kLoadK;
+        const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+        uint8_t* ring = is_k ? ksm : vsm;
+        const int full = is_k ? kBarKFull : kBarVFull, empty = is_k ? kBarKEmpty : kBarVEmpty;
+        if (is_k && lane == 0) {
+            mbar_expect_tx(bar(kBarQ), (uint32_t)(nunits * SM::kQ));
+#pragma unroll 1
+            for (int X = 0; X < nunits; ++X) {
+                const Unit& W = X ? U1 : U0;
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+                    tma_load3(smem_u32(qsm + X * SM::kQ + cb * kRows * 128), &tmap_q, cb * 64, kh * p.g, q0 + W.tok0,
+                              bar(kBarQ));
+            }
+        }
+        __syncwarp();
+        const int32_t* trow = p.tables + (int64_t)s * p.mbps;
+        const int lg_bs = p.bs == 16 ? 4 : 5;
+        const int kt_end = p.stop_tile < 0 ? nkv : min(nkv, p.stop_tile);
+        const int jb = lane / CB, cb = lane % CB;  // this lane's block of a tile and column block
+        bool ok = true;
+        int issued = 0;
+#pragma unroll 1
+        for (int kt = 0; kt < kt_end; ++kt) {
+            const int st = stg(kt);
+            const int tt = tile_token(kt), t = tt + (jb << lg_bs);
+            const bool on = jb < (kTok >> lg_bs) && t < U0.kv_end;
+            int phys = (int)p.num_blocks;  // a block that no row attends: zeros from past the pool
+            if (on && (t < pre || t + p.bs > first)) {
+                phys = __ldg(trow + (t >> lg_bs));
+                if (phys < 0 || phys >= p.num_blocks) {
+                    raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+                    phys = 0;
+                }
+            }
+            const int nbox = __popc(__ballot_sync(kFull, on));
+            if (kt >= kStages) {
+                ok = mbar_wait(bar(empty + st), pass(kt - kStages), abort, p.wait_ns);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+            }
+            if (lane == 0) mbar_expect_tx(bar(full + st), (uint32_t)(nbox * p.bs * 128));
+            __syncwarp();
+            if (on)
+                tma_load3(smem_u32(ring + st * SM::kTile + cb * kTok * 128 + jb * p.bs * 128), map, cb * 64, kh,
+                          phys * p.bs, bar(full + st));
+            ++issued;
+        }
+        if (kt_end < nkv) ok = false;  // (timeout test) the other roles wait for the missing tiles
+        if (!ok) {  // let the copies in flight land before the CTA ends
+            if (is_k) mbar_wait(bar(kBarQ), 0, nullptr, p.wait_ns);
+            for (int kt = max(issued - kStages, 0); kt < issued; ++kt)
+                mbar_wait(bar(full + stg(kt)), pass(kt), nullptr, p.wait_ns);
+        } else if (!is_k && need_fix) {  // zero the last V tile's rows at and past the unit's end
+            const int kl = nkv - 1, st = stg(kl);
+            bool fine = mbar_wait(bar(kBarVFull + st), pass(kl), abort, p.wait_ns);
+            fine = __all_sync(kFull, fine);
+            if (fine) {
+                const int r0 = U0.kv_end - tile_token(kl);
+                uint8_t* vt = vsm + st * SM::kTile;
+                constexpr int CH = D / 8;  // 16-byte chunks per row
+                for (int i = lane; i < (kTok - r0) * CH; i += 32)
+                    *reinterpret_cast<uint4*>(vt + tc_off(r0 + i / CH, i % CH, kTok)) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarVFix));
+            }
+        }
+    }
+    }
+
+    tc_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+    if (tid == 0 && abort_flag) raise_error(p.err, PKV_DEVERR_TIMEOUT);
+}
+
+template <typename T, int D>
+pkv_status launch(const PrefillParams& p, const PfMod& md, const void* query, const void* kc, const void* vc,
+                  int64_t num_tokens, int64_t grid, cudaStream_t st) {
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int kSmem = Smem<T, D>::kBytes;
+    static_assert(kSmem <= 227 * 1024 - 4 * 1024, "shared memory");
+    CUtensorMap tq, tk, tv;
+    pkv_status r = encode_map(&tq, kBf16, query, D, p.num_heads, num_tokens, p.g, kRows / p.g);
+    if (r == PKV_OK) r = encode_map(&tk, kBf16, kc, D, p.num_kv_heads, p.num_blocks * p.bs, 1, p.bs);
+    if (r == PKV_OK) r = encode_map(&tv, kBf16, vc, D, p.num_kv_heads, p.num_blocks * p.bs, 1, p.bs);
+    if (r != PKV_OK) return r;
+    static std::atomic<unsigned long long> configured{0};  // bit per device (< 64)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(PKV_ECUDA, "cudaGetDevice");
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(pkv_prefill_scoremod_kernel<T, D>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return fail(PKV_ECUDA, "prefill smem opt-in: %s", cudaGetErrorString(e));
+        configured.fetch_or(bit);
+    }
+    pkv_prefill_scoremod_kernel<T, D><<<(unsigned)grid, kThreads, kSmem, st>>>(p, tq, tk, tv, md);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "prefill launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status pkv_paged_prefill_scoremod(
+    void* out, const void* query, pkv_dtype q_dtype, const void* key_cache, const void* value_cache,
+    pkv_dtype cache_dtype, const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+    const int32_t* query_start, int num_seqs, int64_t num_query_tokens, int num_heads, int num_kv_heads,
+    int head_dim, int block_size, int64_t num_blocks, float scale, float softcap, int window,
+    const float* alibi_slopes, const int32_t* prefix_lens, pkv_stream_t stream) {
+    PrefillParams p;
+    int64_t grid = 0;
+    pkv_status st = prefill_prepare(&p, &grid, out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables,
+                                    max_blocks_per_seq, seq_lens, query_start, num_seqs, num_query_tokens, num_heads,
+                                    num_kv_heads, head_dim, block_size, num_blocks, scale);
+    if (st != PKV_OK) return st;
+    PfMod md{alibi_slopes, prefix_lens, 0.f, 0.f, window};
+    float inv_cap2 = 0.f;
+    st = score_cap(softcap, &md.cap2, &inv_cap2);
+    if (st != PKV_OK) return st;
+    if (window < 0) return fail(PKV_EINVAL, "window < 0");
+    if (grid == 0) return PKV_OK;
+    md.pre = p.scale_log2 * inv_cap2;
+    if (!(md.pre < INFINITY)) return fail(PKV_EINVAL, "scale / softcap overflows fp32");
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t T = num_query_tokens;
+    if (cache_dtype == PKV_F16)
+        return head_dim == 64 ? launch<__half, 64>(p, md, query, key_cache, value_cache, T, grid, cs)
+                              : launch<__half, 128>(p, md, query, key_cache, value_cache, T, grid, cs);
+    return head_dim == 64 ? launch<__nv_bfloat16, 64>(p, md, query, key_cache, value_cache, T, grid, cs)
+                          : launch<__nv_bfloat16, 128>(p, md, query, key_cache, value_cache, T, grid, cs);
+}

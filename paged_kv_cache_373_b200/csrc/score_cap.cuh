@@ -45,4 +45,31 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], float pre, float cap2)
     }
 }
 
+// The same without the final factor, N scores by pairs: x -> tanh(x pre).
+template <int N>
+__device__ __forceinline__ void cap_pairs(float (&x)[N], float pre) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(x[i]));
+    const F2 p2 = f2(pre, pre);
+    if (big * pre < 0.5f) {
+        const F2 c4 = f2(0.01724149100482464f, 0.01724149100482464f), c3 = f2(-0.05304549261927605f, -0.05304549261927605f),
+                 c2 = f2(0.13325878977775574f, 0.13325878977775574f), c1 = f2(-0.333331435918808f, -0.333331435918808f);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {  // tanh_poly on two values
+            const F2 y = f2_mul(f2(x[i], x[i + 1]), p2), z = f2_mul(y, y);
+            const F2 q = f2_fma(z, f2_fma(z, f2_fma(z, c4, c3), c2), c1);
+            const float2 r = f2_get(f2_fma(f2_mul(y, z), q, y));
+            x[i] = r.x;
+            x[i + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float y = x[i] * pre;
+            x[i] = fabsf(y) < 0.5f ? tanh_poly(y) : tanh_exp(y);
+        }
+    }
+}
+
 }  // namespace pkv
