@@ -6,20 +6,20 @@
 //
 // Unit: (sequence, kv head, 128 query rows), a row being a (chunk token, q head
 // of the kv head's group) pair; a CTA takes two adjacent units of one (sequence,
-// kv head), which read the same K/V tiles of 128 tokens, and keeps the tensor
-// core on one unit while the other runs its softmax:
+// kv head), which read the same K/V tiles of 64 tokens:
 //   - warps 0-3 and 4-7: the units' softmax, one thread per row, so that a row's
-//     maximum and sum need no exchange: all 128 scores of a tile come from tensor
-//     memory in one load, are capped, biased and masked in registers (by pairs,
-//     fp32x2), exponentiated against a reference maximum, and P goes back over the
-//     scores (bf16 as hi + lo parts: 64 + 64 columns, exactly the 128 of S), where
-//     the P V product reads it as its A operand.  O stays in tensor memory and is
-//     rescaled only when a row's maximum passes its reference by 2^8;
-//   - warp 8 (one lane) owns tensor memory (S_0, S_1, O_0, O_1: 512 columns) and
-//     issues, per tile, O_0 += P_0 V, S_0' = Q_0 K'^T, O_1 += P_1 V, S_1' = Q_1 K'^T.
-//     Products issued by one thread run in order, so S' may overwrite the P that the
-//     product before it reads, and a finished S' says that O is settled;
-//   - warps 9 and 10 copy the K and the V tiles (2-stage rings) with TMA through the
+//     maximum and sum need no exchange: the 64 scores of a tile come from tensor
+//     memory in one load, are capped, biased and masked in registers, exponentiated
+//     against a reference maximum (by pairs, fp32x2), and P goes back over the scores
+//     (bf16 as hi + lo parts: 32 + 32 columns, exactly the 64 of S), where the P V
+//     product reads it as its A operand.  Every unit has two S buffers, so the scores
+//     of the next tile are ready when a tile's P is done.  O stays in tensor memory and
+//     is rescaled only when a row's maximum passes its reference by 2^8;
+//   - warp 8 (one lane) owns tensor memory (per unit two S of 64 and an O of
+//     head_dim columns) and issues, per tile, O_0 += P_0 V, S_0'' = Q_0 K''^T, O_1 += P_1 V,
+//     S_1'' = Q_1 K''^T (the tile after the next).  Products issued by one thread run in
+//     order, so S'' may overwrite the P that the product before it reads;
+//   - warps 9 and 10 copy the K and the V tiles (4-stage rings) with TMA through the
 //     block table, a lane per box.
 // A pair's tiles are those that hold its prefix and then those from its earliest
 // row's window on; the tiles between (tile kt of the walk is tile kt of the sequence
@@ -53,18 +53,12 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;          // query rows per unit (tensor-core M)
-constexpr int kTok = 128;           // KV tokens per tile (N of S, K of P V)
-constexpr int kStages = 2;          // K and V ring depth
+constexpr int kTok = 64;            // KV tokens per tile (N of S, K of P V)
+constexpr int kStages = 4;          // K and V ring depth
 constexpr int kSoftWarps = 8;       // 4 per unit: a thread per row
-constexpr int kMmaWarp = 8, kLoadK = 9, kLoadV = 10;
-constexpr int kThreads = 12 * 32;   // (warp 11 only fills the last register group)
-// Registers per thread: the launch's 168 (12 warps of 168 are what an SM has),
-// shifted from the issuing warps to the softmax warps, which hold a whole row of
-// scores: 2 * 128 * 224 + 128 * 56 = 384 * 168.
-constexpr int kRegsSoft = 224, kRegsIssue = 56, kRegsLaunch = 168;
-static_assert(kSoftWarps * kRegsSoft + (kThreads / 32 - kSoftWarps) * kRegsIssue == kThreads / 32 * kRegsLaunch,
-              "the shares add up to the launch's registers");
-constexpr int kTmemCols = 512;      // S_X in columns 128 X.., O_X from 256 + 128 X
+constexpr int kMmaWarp = 8, kLoadK = 9;  // and the V tiles by warp 10
+constexpr int kThreads = 11 * 32;
+constexpr int kTmemCols = 512;      // S_X in columns 128 X + 64 (tile & 1).., O_X from 256 + 128 X
 
 enum : int {
     kBarQ = 0,                         // q rows landed
@@ -73,19 +67,25 @@ enum : int {
     kBarKEmpty = kBarVFull + kStages,  // [stage] every S product of the K stage finished
     kBarVEmpty = kBarKEmpty + kStages, // [stage] every P V product of the V stage finished
     kBarVFix = kBarVEmpty + kStages,   // the last V tile's rows past the unit's end are zeroed
-    kBarS = kBarVFix + 1,              // [unit] S ready (and O settled)
-    kBarP = kBarS + 2,                 // [unit] P written: kRows arrivals
-    kBarO = kBarP + 2,                 // [unit] the last P V finished
-    kBarDrain = kBarO + 2,             // products drained
+    kBarS = kBarVFix + 1,              // [unit][buffer] S ready
+    kBarP = kBarS + 4,                 // [unit][buffer] P written: kRows arrivals
+    kBarO = kBarP + 4,                 // [unit] a tile's P V finished
+    kBarEnd = kBarO + 2,               // [unit] its last P V finished
+    kBarDrain = kBarEnd + 2,           // products drained
     kNumBars = kBarDrain + 1
 };
 
 struct PfMod {
     const float* slopes;         // [num_heads] or null
     const int32_t* prefix_lens;  // [num_seqs] or null
-    float cap2, pre;             // cap log2(e) (0: no cap), scale / cap
+    float pre;                   // scale / cap (0: no cap)
     int window;                  // 0: no window
 };
+
+// The first n of a tile's 64 columns (none for n <= 0).
+__device__ __forceinline__ uint64_t columns_below(int n) {
+    return n <= 0 ? 0ull : n >= kTok ? ~0ull : (1ull << n) - 1;
+}
 
 struct Unit {
     int tok0, ntok, pos0, kv_end, nkv;
@@ -213,7 +213,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
     }
     if (tid == 0) {
-        for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i == kBarP || i == kBarP + 1) ? kRows : 1);
+        for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= kBarP && i < kBarP + 4 ? kRows : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_flag = 0;
     }
@@ -224,7 +224,6 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
     if (warp < kSoftWarps) {
         // ================= softmax group X: unit X (or, for a unit alone, its
         // tiles of parity X), a thread per row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int X = warp >> 2;
         const Unit U = X && !split ? U1 : U0;
         const int kt0 = split ? X : 0, kstep = split ? 2 : 1;  // this group's tiles
@@ -233,20 +232,20 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         const int pos = (row / p.g < U.ntok) ? U.pos0 + row / p.g : -1;
         const int last = U.pos0 + U.ntok - 1;
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_addr + X * kTok;
+        const uint32_t tS = tmem + lane_addr + X * 128;
         const uint32_t tO = tmem + lane_addr + 256 + X * 128;
-        const bool capped = md.cap2 > 0.f, biased = md.slopes != nullptr;
-        // scores leave the cap as tanh values; without a bias their last factor
-        // is applied in the exponent
-        const float mult = capped ? md.cap2 : p.scale_log2;
-        const float emul = biased ? 1.f : mult;
+        const bool capped = md.pre > 0.f, biased = md.slopes != nullptr;
+        const CapCoef cap = cap_coef(capped ? md.pre : 1.f);
+        const float sl2 = p.scale_log2;
+        const float emul = biased ? 1.f : sl2;  // without a bias the scale is applied in the exponent
         const float slope2 = biased ? __ldg(md.slopes + (int64_t)kh * p.g + row % p.g) * 1.4426950408889634f : 0.f;
         float mref = -INFINITY, l = 0.f;  // reference maximum (log2 domain) and sum of the row
         bool failed = false;
 #pragma unroll 1
         for (int i = 0; i < ntiles; ++i) {
-            const int tt = tile_token(kt0 + i * kstep);
-            bool ok = mbar_wait(bar(kBarS + X), i & 1, abort, p.wait_ns);
+            const int tt = tile_token(kt0 + i * kstep), buf = i & 1;
+            const uint32_t tSb = tS + buf * kTok;
+            bool ok = mbar_wait(bar(kBarS + 2 * X + buf), (i >> 1) & 1, abort, p.wait_ns);
             ok = __all_sync(kFull, ok);
             if (!ok) {
                 failed = true;
@@ -254,19 +253,23 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             }
             tc_after_sync();
             float sc[kTok];
-            tc_ld128(tS, sc);
-            if (capped) cap_pairs(sc, md.pre);
+            tc_ld64(tSb, sc);
+            if (capped) cap_pairs(sc, cap);
             if (biased) {
                 const float d0 = (float)(pos - tt);
 #pragma unroll
-                for (int c = 0; c < kTok; ++c) sc[c] = fmaf(sc[c], mult, -slope2 * fabsf(d0 - (float)c));
+                for (int c = 0; c < kTok; ++c) sc[c] = fmaf(sc[c], sl2, -slope2 * fabsf(d0 - (float)c));
             }
             // tiles with a token past the first row, or at or before the last row's window
             if (tt + kTok - 1 > U.pos0 || (window > 0 && tt <= last - window)) {
-                // columns attended: below `pc`, or in [lo, hi]
-                const int pc = pre - tt, hi = pos - tt, lo = window > 0 ? pos - window + 1 - tt : -tt;
+                const uint64_t vis = columns_below(pre - tt) |
+                                     (columns_below(pos - tt + 1) & ~(window > 0 ? columns_below(pos - window + 1 - tt) : 0ull));
+                const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
-                for (int c = 0; c < kTok; ++c) sc[c] = c < pc || (c <= hi && c >= lo) ? sc[c] : -INFINITY;
+                for (int c = 0; c < 32; ++c) {
+                    sc[c] = v0 & (1u << c) ? sc[c] : -INFINITY;
+                    sc[32 + c] = v1 & (1u << c) ? sc[32 + c] : -INFINITY;
+                }
             }
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -279,7 +282,14 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                 l *= alpha;
                 mref = mx;
             }
-            if (i > 0 && __any_sync(kFull, grow)) {  // rescale O (settled: S of this tile was issued after it)
+            if (i > 0 && __any_sync(kFull, grow)) {  // rescale O, once the previous tile's product is in it
+                ok = mbar_wait(bar(kBarO + X), (i - 1) & 1, abort, p.wait_ns);
+                ok = __all_sync(kFull, ok);
+                if (!ok) {
+                    failed = true;
+                    break;
+                }
+                tc_after_sync();
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 16) {
                     float v[16];
@@ -308,19 +318,19 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                         lo[e] = pack2<true>(r.x, r.y);
                     }
                 }
-                tc_st16u(tS + c0 / 2, h);
-                if constexpr (kBf16) tc_st16u(tS + kTok / 2 + c0 / 2, lo);
+                tc_st16u(tSb + c0 / 2, h);
+                if constexpr (kBf16) tc_st16u(tSb + kTok / 2 + c0 / 2, lo);
             }
             const float2 s2 = f2_get(f2_add(sum[0], sum[1]));
             l += s2.x + s2.y;
             tc_wait_st();
             tc_before_sync();
-            mbar_arrive(bar(kBarP + X));
+            mbar_arrive(bar(kBarP + 2 * X + buf));
         }
         // ---- the last P V, then normalise (a split unit also merges group 1's
         // partial result) and store
-        bool ok = !failed && (ntiles == 0 || mbar_wait(bar(kBarO + X), 0, abort, p.wait_ns));
-        if (split && X == 0 && nkv > 1) ok = ok && mbar_wait(bar(kBarO + 1), 0, abort, p.wait_ns);  // read in the merge
+        bool ok = !failed && (ntiles == 0 || mbar_wait(bar(kBarEnd + X), 0, abort, p.wait_ns));
+        if (split && X == 0 && nkv > 1) ok = ok && mbar_wait(bar(kBarEnd + 1), 0, abort, p.wait_ns);  // read in the merge
         ok = __all_sync(kFull, ok);
         bool merge = false;
         if (split) {
@@ -367,9 +377,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                 }
             }
         }
-    } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp) {
         // ================= tensor-core issue (one lane)
         if (lane == 0) {
             const uint32_t id_s = tc_idesc<kBf16>(kRows, kTok, 0);
@@ -378,94 +386,104 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             const uint64_t dq1 = tc_desc(smem_u32(qsm + (split ? 0 : SM::kQ)), 16, 1024);
             const uint64_t dk0 = tc_desc(smem_u32(ksm), 16, 1024);
             const uint64_t dv0 = tc_desc(smem_u32(vsm), kTok * 128, 1024);
-            auto issue_s = [&](int X, int st) {  // S_X = Q_X K^T (a split unit: both groups read q slot 0)
+            // S_X = Q_X K^T into buffer b (a split unit: both groups read q slot 0)
+            auto issue_s = [&](int X, int b, int st) {
                 const uint64_t qd = X ? dq1 : dq0;
                 const uint64_t kd = desc_add(dk0, (uint32_t)(st * (SM::kTile >> 4)));
-                const uint32_t d = tmem + X * kTok;
+                const uint32_t d = tmem + X * 128 + b * kTok;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     tc_mma(d, desc_add(qd, ((kk >> 2) * kRows * 128 + (kk & 3) * 32) >> 4),
                            desc_add(kd, ((kk >> 2) * kTok * 128 + (kk & 3) * 32) >> 4), id_s, kk > 0);
-                tc_commit(bar(kBarS + X));
+                tc_commit(bar(kBarS + 2 * X + b));
             };
-            auto issue_pv = [&](int X, int st, bool acc) {  // O_X (+)= P_X V (hi, then lo; P over S_X)
+            // O_X (+)= P_X V (hi, then lo; P over S_X in buffer b)
+            auto issue_pv = [&](int X, int b, int st, bool acc) {
                 const uint64_t vd = desc_add(dv0, (uint32_t)(st * (SM::kTile >> 4)));
-                const uint32_t d = tmem + 256 + X * 128, a = tmem + X * kTok;
+                const uint32_t d = tmem + 256 + X * 128, a = tmem + X * 128 + b * kTok;
 #pragma unroll
                 for (int part = 0; part < SM::kParts; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kTok / 16; ++kk)
                         tc_mma_ts(d, a + part * (kTok / 2) + kk * 8, desc_add(vd, (kk * 2048) >> 4), id_o,
                                   (acc || part > 0 || kk > 0) ? 1u : 0u);
+                tc_commit(bar(kBarO + X));
             };
             bool ok = mbar_wait(bar(kBarQ), 0, abort, p.wait_ns);
             if (!split) {
-                ok = ok && mbar_wait(bar(kBarKFull), 0, abort, p.wait_ns);
-                if (ok) {
-                    tc_after_sync();
-                    issue_s(0, 0);
-                    issue_s(1, 0);
-                    tc_commit(bar(kBarKEmpty));
+                // paired units: every tile serves both; per tile kt
+                // O_0 += P_0 V, S_0 of tile kt + 2, O_1 += P_1 V, S_1 of tile kt + 2
+                auto wait_k = [&](int kt) {
+                    const bool r = mbar_wait(bar(kBarKFull + stg(kt)), pass(kt), abort, p.wait_ns);
+                    if (r) tc_after_sync();
+                    return r;
+                };
+#pragma unroll 1
+                for (int kt = 0; ok && kt < 2 && kt < nkv; ++kt) {
+                    ok = wait_k(kt);
+                    if (!ok) break;
+                    issue_s(0, kt, stg(kt));
+                    if (kt < U1.nkv) issue_s(1, kt, stg(kt));
+                    tc_commit(bar(kBarKEmpty + stg(kt)));
                 }
 #pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
-                    const int st = stg(kt), sn = stg(kt + 1);
-                    const bool a1 = kt < U1.nkv, a1n = kt + 1 < U1.nkv;
+                    const int st = stg(kt), sn = stg(kt + 2), b = kt & 1;
+                    const bool a1 = kt < U1.nkv, a1n = kt + 2 < U1.nkv;
                     ok = mbar_wait(bar(kBarVFull + st), pass(kt), abort, p.wait_ns) &&
                          (kt != nkv - 1 || !need_fix || mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) &&
-                         mbar_wait(bar(kBarP), kt & 1, abort, p.wait_ns);
+                         mbar_wait(bar(kBarP + b), (kt >> 1) & 1, abort, p.wait_ns);
                     if (!ok) break;
                     tc_after_sync();
-                    issue_pv(0, st, kt > 0);
-                    if (kt == nkv - 1) tc_commit(bar(kBarO));
+                    issue_pv(0, b, st, kt > 0);
+                    if (kt == nkv - 1) tc_commit(bar(kBarEnd));
                     if (!a1) tc_commit(bar(kBarVEmpty + st));
-                    if (kt + 1 < nkv) {
-                        ok = mbar_wait(bar(kBarKFull + sn), pass(kt + 1), abort, p.wait_ns);
+                    if (kt + 2 < nkv) {
+                        ok = wait_k(kt + 2);
                         if (!ok) break;
-                        tc_after_sync();
-                        issue_s(0, sn);
+                        issue_s(0, b, sn);
                         if (!a1n) tc_commit(bar(kBarKEmpty + sn));
                     }
                     if (a1) {
-                        ok = mbar_wait(bar(kBarP + 1), kt & 1, abort, p.wait_ns);
+                        ok = mbar_wait(bar(kBarP + 2 + b), (kt >> 1) & 1, abort, p.wait_ns);
                         if (!ok) break;
                         tc_after_sync();
-                        issue_pv(1, st, kt > 0);
-                        if (!a1n) tc_commit(bar(kBarO + 1));
+                        issue_pv(1, b, st, kt > 0);
+                        if (kt == U1.nkv - 1) tc_commit(bar(kBarEnd + 1));
                         tc_commit(bar(kBarVEmpty + st));
                         if (a1n) {
-                            issue_s(1, sn);
+                            issue_s(1, b, sn);
                             tc_commit(bar(kBarKEmpty + sn));
                         }
                     }
                 }
             } else {
-                // a split unit: group X takes tiles 2 i + X
+                // a split unit: group X = kt & 1 takes tile kt into its buffer (kt >> 1) & 1
 #pragma unroll 1
-                for (int kt = 0; ok && kt < 2 && kt < nkv; ++kt) {
+                for (int kt = 0; ok && kt < 4 && kt < nkv; ++kt) {
                     ok = mbar_wait(bar(kBarKFull + stg(kt)), pass(kt), abort, p.wait_ns);
                     if (!ok) break;
                     tc_after_sync();
-                    issue_s(kt, stg(kt));
+                    issue_s(kt & 1, kt >> 1, stg(kt));
                     tc_commit(bar(kBarKEmpty + stg(kt)));
                 }
 #pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
-                    const int X = kt & 1;
+                    const int X = kt & 1, b = (kt >> 1) & 1;
                     ok = mbar_wait(bar(kBarVFull + stg(kt)), pass(kt), abort, p.wait_ns) &&
                          (kt != nkv - 1 || !need_fix || mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) &&
-                         mbar_wait(bar(kBarP + X), (kt >> 1) & 1, abort, p.wait_ns);
+                         mbar_wait(bar(kBarP + 2 * X + b), (kt >> 2) & 1, abort, p.wait_ns);
                     if (!ok) break;
                     tc_after_sync();
-                    issue_pv(X, stg(kt), kt > 1);
-                    if (kt + 2 >= nkv) tc_commit(bar(kBarO + X));
+                    issue_pv(X, b, stg(kt), kt > 1);
+                    if (kt + 2 >= nkv) tc_commit(bar(kBarEnd + X));
                     tc_commit(bar(kBarVEmpty + stg(kt)));
-                    if (kt + 2 < nkv) {
-                        ok = mbar_wait(bar(kBarKFull + stg(kt + 2)), pass(kt + 2), abort, p.wait_ns);
+                    if (kt + 4 < nkv) {
+                        ok = mbar_wait(bar(kBarKFull + stg(kt + 4)), pass(kt + 4), abort, p.wait_ns);
                         if (!ok) break;
                         tc_after_sync();
-                        issue_s(X, stg(kt + 2));
-                        tc_commit(bar(kBarKEmpty + stg(kt + 2)));
+                        issue_s(X, b, stg(kt + 4));
+                        tc_commit(bar(kBarKEmpty + stg(kt + 4)));
                     }
                 }
             }
@@ -473,9 +491,9 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             mbar_wait(bar(kBarDrain), 0, nullptr, p.wait_ns);
         }
         __syncwarp();
-    } else if (warp <= kLoadV) {
+    } else {
         // ================= TMA copies: warp kLoadK the q rows and the K tiles,
-        // warp kLoadV the V tiles; a lane per 64-element box
+        // the next warp the V tiles; a lane per 64-element box
         const bool is_k = warp == kLoadK;
         const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
         uint8_t* ring = is_k ? ksm : vsm;
@@ -545,7 +563,6 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             }
         }
     }
-    }
 
     tc_before_sync();
     __syncthreads();
@@ -600,14 +617,18 @@ extern "C" pkv_status pkv_paged_prefill_scoremod(
                                     max_blocks_per_seq, seq_lens, query_start, num_seqs, num_query_tokens, num_heads,
                                     num_kv_heads, head_dim, block_size, num_blocks, scale);
     if (st != PKV_OK) return st;
-    PfMod md{alibi_slopes, prefix_lens, 0.f, 0.f, window};
-    float inv_cap2 = 0.f;
-    st = score_cap(softcap, &md.cap2, &inv_cap2);
+    PfMod md{alibi_slopes, prefix_lens, 0.f, window};
+    float cap2 = 0.f, inv_cap2 = 0.f;
+    st = score_cap(softcap, &cap2, &inv_cap2);
     if (st != PKV_OK) return st;
     if (window < 0) return fail(PKV_EINVAL, "window < 0");
+    if ((int64_t)max_blocks_per_seq * block_size > 0x40000000LL)  // positions and windows add up in 32 bits
+        return fail(PKV_EUNSUPPORTED, "table rows of more than 2^30 tokens");
+    if (window >= max_blocks_per_seq * block_size) md.window = 0;  // hides nothing
     if (grid == 0) return PKV_OK;
     md.pre = p.scale_log2 * inv_cap2;
-    if (!(md.pre < INFINITY)) return fail(PKV_EINVAL, "scale / softcap overflows fp32");
+    if (softcap > 0.f && !(md.pre > 0.f && 1.f / md.pre > 0.f && 1.f / md.pre < INFINITY && md.pre < INFINITY))
+        return fail(PKV_EINVAL, "scale / softcap outside fp32");
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const int64_t T = num_query_tokens;
     if (cache_dtype == PKV_F16)
