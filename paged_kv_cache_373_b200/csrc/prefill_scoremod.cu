@@ -82,6 +82,30 @@ struct PfMod {
     int window;                  // 0: no window
 };
 
+// The tensor-core instructions of the issuing warp: every lane runs its loop, so
+// that control flow is uniform and the descriptors stay in uniform registers,
+// and the elected lane's predicate is on the instruction itself.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on));
+}
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on));
+}
+__device__ __forceinline__ void commit(uint32_t on, uint32_t mbar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+                 ::"r"(mbar), "r"(on) : "memory");
+}
+
 // The first n of a tile's 64 columns (none for n <= 0).
 __device__ __forceinline__ uint64_t columns_below(int n) {
     return n <= 0 ? 0ull : n >= kTok ? ~0ull : (1ull << n) - 1;
@@ -378,8 +402,12 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             }
         }
     } else if (warp == kMmaWarp) {
-        // ================= tensor-core issue (one lane)
-        if (lane == 0) {
+        // ================= tensor-core issue
+        {
+            const uint32_t on = elect_one();
+            auto wait = [&](int i, uint32_t parity) {
+                return __all_sync(kFull, mbar_wait(bar(i), parity, abort, p.wait_ns)) != 0;
+            };
             const uint32_t id_s = tc_idesc<kBf16>(kRows, kTok, 0);
             const uint32_t id_o = tc_idesc<kBf16>(kRows, D, 1);
             const uint64_t dq0 = tc_desc(smem_u32(qsm), 16, 1024);
@@ -393,9 +421,9 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                 const uint32_t d = tmem + X * 128 + b * kTok;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma(d, desc_add(qd, ((kk >> 2) * kRows * 128 + (kk & 3) * 32) >> 4),
+                    mma_ss(on, d, desc_add(qd, ((kk >> 2) * kRows * 128 + (kk & 3) * 32) >> 4),
                            desc_add(kd, ((kk >> 2) * kTok * 128 + (kk & 3) * 32) >> 4), id_s, kk > 0);
-                tc_commit(bar(kBarS + 2 * X + b));
+                commit(on, bar(kBarS + 2 * X + b));
             };
             // O_X (+)= P_X V (hi, then lo; P over S_X in buffer b)
             auto issue_pv = [&](int X, int b, int st, bool acc) {
@@ -405,16 +433,16 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                 for (int part = 0; part < SM::kParts; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kTok / 16; ++kk)
-                        tc_mma_ts(d, a + part * (kTok / 2) + kk * 8, desc_add(vd, (kk * 2048) >> 4), id_o,
+                        mma_ts(on, d, a + part * (kTok / 2) + kk * 8, desc_add(vd, (kk * 2048) >> 4), id_o,
                                   (acc || part > 0 || kk > 0) ? 1u : 0u);
-                tc_commit(bar(kBarO + X));
+                commit(on, bar(kBarO + X));
             };
-            bool ok = mbar_wait(bar(kBarQ), 0, abort, p.wait_ns);
+            bool ok = wait(kBarQ, 0);
             if (!split) {
                 // paired units: every tile serves both; per tile kt
                 // O_0 += P_0 V, S_0 of tile kt + 2, O_1 += P_1 V, S_1 of tile kt + 2
                 auto wait_k = [&](int kt) {
-                    const bool r = mbar_wait(bar(kBarKFull + stg(kt)), pass(kt), abort, p.wait_ns);
+                    const bool r = wait(kBarKFull + stg(kt), pass(kt));
                     if (r) tc_after_sync();
                     return r;
                 };
@@ -424,36 +452,36 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                     if (!ok) break;
                     issue_s(0, kt, stg(kt));
                     if (kt < U1.nkv) issue_s(1, kt, stg(kt));
-                    tc_commit(bar(kBarKEmpty + stg(kt)));
+                    commit(on, bar(kBarKEmpty + stg(kt)));
                 }
 #pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
                     const int st = stg(kt), sn = stg(kt + 2), b = kt & 1;
                     const bool a1 = kt < U1.nkv, a1n = kt + 2 < U1.nkv;
-                    ok = mbar_wait(bar(kBarVFull + st), pass(kt), abort, p.wait_ns) &&
-                         (kt != nkv - 1 || !need_fix || mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) &&
-                         mbar_wait(bar(kBarP + b), (kt >> 1) & 1, abort, p.wait_ns);
+                    ok = wait(kBarVFull + st, pass(kt)) &&
+                         (kt != nkv - 1 || !need_fix || wait(kBarVFix, 0)) &&
+                         wait(kBarP + b, (kt >> 1) & 1);
                     if (!ok) break;
                     tc_after_sync();
                     issue_pv(0, b, st, kt > 0);
-                    if (kt == nkv - 1) tc_commit(bar(kBarEnd));
-                    if (!a1) tc_commit(bar(kBarVEmpty + st));
+                    if (kt == nkv - 1) commit(on, bar(kBarEnd));
+                    if (!a1) commit(on, bar(kBarVEmpty + st));
                     if (kt + 2 < nkv) {
                         ok = wait_k(kt + 2);
                         if (!ok) break;
                         issue_s(0, b, sn);
-                        if (!a1n) tc_commit(bar(kBarKEmpty + sn));
+                        if (!a1n) commit(on, bar(kBarKEmpty + sn));
                     }
                     if (a1) {
-                        ok = mbar_wait(bar(kBarP + 2 + b), (kt >> 1) & 1, abort, p.wait_ns);
+                        ok = wait(kBarP + 2 + b, (kt >> 1) & 1);
                         if (!ok) break;
                         tc_after_sync();
                         issue_pv(1, b, st, kt > 0);
-                        if (kt == U1.nkv - 1) tc_commit(bar(kBarEnd + 1));
-                        tc_commit(bar(kBarVEmpty + st));
+                        if (kt == U1.nkv - 1) commit(on, bar(kBarEnd + 1));
+                        commit(on, bar(kBarVEmpty + st));
                         if (a1n) {
                             issue_s(1, b, sn);
-                            tc_commit(bar(kBarKEmpty + sn));
+                            commit(on, bar(kBarKEmpty + sn));
                         }
                     }
                 }
@@ -461,33 +489,33 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                 // a split unit: group X = kt & 1 takes tile kt into its buffer (kt >> 1) & 1
 #pragma unroll 1
                 for (int kt = 0; ok && kt < 4 && kt < nkv; ++kt) {
-                    ok = mbar_wait(bar(kBarKFull + stg(kt)), pass(kt), abort, p.wait_ns);
+                    ok = wait(kBarKFull + stg(kt), pass(kt));
                     if (!ok) break;
                     tc_after_sync();
                     issue_s(kt & 1, kt >> 1, stg(kt));
-                    tc_commit(bar(kBarKEmpty + stg(kt)));
+                    commit(on, bar(kBarKEmpty + stg(kt)));
                 }
 #pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
                     const int X = kt & 1, b = (kt >> 1) & 1;
-                    ok = mbar_wait(bar(kBarVFull + stg(kt)), pass(kt), abort, p.wait_ns) &&
-                         (kt != nkv - 1 || !need_fix || mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) &&
-                         mbar_wait(bar(kBarP + 2 * X + b), (kt >> 2) & 1, abort, p.wait_ns);
+                    ok = wait(kBarVFull + stg(kt), pass(kt)) &&
+                         (kt != nkv - 1 || !need_fix || wait(kBarVFix, 0)) &&
+                         wait(kBarP + 2 * X + b, (kt >> 2) & 1);
                     if (!ok) break;
                     tc_after_sync();
                     issue_pv(X, b, stg(kt), kt > 1);
-                    if (kt + 2 >= nkv) tc_commit(bar(kBarEnd + X));
-                    tc_commit(bar(kBarVEmpty + stg(kt)));
+                    if (kt + 2 >= nkv) commit(on, bar(kBarEnd + X));
+                    commit(on, bar(kBarVEmpty + stg(kt)));
                     if (kt + 4 < nkv) {
-                        ok = mbar_wait(bar(kBarKFull + stg(kt + 4)), pass(kt + 4), abort, p.wait_ns);
+                        ok = wait(kBarKFull + stg(kt + 4), pass(kt + 4));
                         if (!ok) break;
                         tc_after_sync();
                         issue_s(X, b, stg(kt + 4));
-                        tc_commit(bar(kBarKEmpty + stg(kt + 4)));
+                        commit(on, bar(kBarKEmpty + stg(kt + 4)));
                     }
                 }
             }
-            tc_commit(bar(kBarDrain));  // every product issued has finished before tensor memory is freed
+            commit(on, bar(kBarDrain));  // every product issued has finished before tensor memory is freed
             mbar_wait(bar(kBarDrain), 0, nullptr, p.wait_ns);
         }
         __syncwarp();
