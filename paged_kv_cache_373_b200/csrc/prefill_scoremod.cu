@@ -20,7 +20,8 @@
 //     S_1'' = Q_1 K''^T (the tile after the next).  Products issued by one thread run in
 //     order, so S'' may overwrite the P that the product before it reads;
 //   - warps 9 and 10 copy the K and the V tiles (4-stage rings) with TMA through the
-//     block table, a lane per box.
+//     block table, a lane per box; warp 11 turns the copies' mbarriers into counters,
+//     which warp 8 reads together with the softmax warps'.
 // A pair's tiles are those that hold its prefix and then those from its earliest
 // row's window on; the tiles between (tile kt of the walk is tile kt of the sequence
 // up to the prefix's last, kt + gap after it) are left out.  A block of a walked tile
@@ -56,8 +57,8 @@ constexpr int kRows = 128;          // query rows per unit (tensor-core M)
 constexpr int kTok = 64;            // KV tokens per tile (N of S, K of P V)
 constexpr int kStages = 4;          // K and V ring depth
 constexpr int kSoftWarps = 8;       // 4 per unit: a thread per row
-constexpr int kMmaWarp = 8, kLoadK = 9;  // and the V tiles by warp 10
-constexpr int kThreads = 11 * 32;
+constexpr int kMmaWarp = 8, kLoadK = 9, kWatchWarp = 11;  // (the V tiles: warp 10)
+constexpr int kThreads = 12 * 32;
 constexpr int kTmemCols = 512;      // S_X in columns 128 X + 64 (tile & 1).., O_X from 256 + 128 X
 
 enum : int {
@@ -68,11 +69,20 @@ enum : int {
     kBarVEmpty = kBarKEmpty + kStages, // [stage] every P V product of the V stage finished
     kBarVFix = kBarVEmpty + kStages,   // the last V tile's rows past the unit's end are zeroed
     kBarS = kBarVFix + 1,              // [unit][buffer] S ready
-    kBarP = kBarS + 4,                 // [unit][buffer] P written: kRows arrivals
-    kBarO = kBarP + 4,                 // [unit] a tile's P V finished
+    kBarO = kBarS + 4,                 // [unit] a tile's P V finished
     kBarEnd = kBarO + 2,               // [unit] its last P V finished
     kBarDrain = kBarEnd + 2,           // products drained
     kNumBars = kBarDrain + 1
+};
+
+// What the issuing warp waits for, as counters in shared memory that one load of
+// the warp reads together (a wait on a finished mbarrier phase costs it 200 cycles,
+// and it would need four per tile):
+enum : int {
+    kCntP = 0,  // [unit][softmax warp] tiles whose P is written
+    kCntK = 8,  // K tiles landed (copied on from the mbarriers by kWatchWarp)
+    kCntV = 9,  // V tiles landed, the last one's rows past the end zeroed
+    kNumCnt = 16
 };
 
 struct PfMod {
@@ -104,6 +114,10 @@ __device__ __forceinline__ void commit(uint32_t on, uint32_t mbar) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
                  ::"r"(mbar), "r"(on) : "memory");
+}
+
+__device__ __forceinline__ void publish(uint32_t addr, int n) {
+    asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(addr), "r"(n) : "memory");
 }
 
 // The first n of a tile's 64 columns (none for n <= 0).
@@ -150,6 +164,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
     __shared__ __align__(8) uint64_t bars[kNumBars];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
+    __shared__ int counters[kNumCnt];
     __shared__ float xsum[kRows], xref[kRows];  // group 1's row sums and references (split unit)
     volatile int* abort = &abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -237,7 +252,8 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
     }
     if (tid == 0) {
-        for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= kBarP && i < kBarP + 4 ? kRows : 1);
+        for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i < kNumCnt; ++i) counters[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_flag = 0;
     }
@@ -349,7 +365,8 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             l += s2.x + s2.y;
             tc_wait_st();
             tc_before_sync();
-            mbar_arrive(bar(kBarP + 2 * X + buf));
+            __syncwarp();
+            if (lane == 0) publish(smem_u32(&counters[kCntP + warp]), i + 1);
         }
         // ---- the last P V, then normalise (a split unit also merges group 1's
         // partial result) and store
@@ -405,8 +422,35 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         // ================= tensor-core issue
         {
             const uint32_t on = elect_one();
-            auto wait = [&](int i, uint32_t parity) {
-                return __all_sync(kFull, mbar_wait(bar(i), parity, abort, p.wait_ns)) != 0;
+            // wait until every lane's counter has reached the lane's target
+            // (bounded as mbar_wait)
+            const uint32_t cnt = smem_u32(&counters[min(lane, kNumCnt - 1)]);
+            constexpr int kNone = -1;  // a counter that does not matter
+            auto reached = [&](int target) {
+                uint64_t t0 = 0;
+                for (uint32_t it = 1;; ++it) {
+                    int v;
+                    asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(cnt) : "memory");
+                    if (__all_sync(kFull, v >= target)) {
+                        __syncwarp();  // what any lane acquired, the issuing lane has
+                        tc_after_sync();
+                        return true;
+                    }
+                    if ((it & 255) == 0) {
+                        bool stop = *abort != 0;
+                        const uint64_t now = global_ns();
+                        if (t0 == 0) t0 = now;
+                        else if (now - t0 > p.wait_ns) stop = true;
+                        if (__any_sync(kFull, stop)) {
+                            if (lane == 0) *abort = 1;
+                            return false;
+                        }
+                    }
+                }
+            };
+            // this lane's target for P of unit X, K and V tiles (as counts)
+            auto target = [&](int X, int np, int nk, int nv) {
+                return lane < kCntK ? (lane >> 2 == X ? np : kNone) : lane == kCntK ? nk : lane == kCntV ? nv : kNone;
             };
             const uint32_t id_s = tc_idesc<kBf16>(kRows, kTok, 0);
             const uint32_t id_o = tc_idesc<kBf16>(kRows, D, 1);
@@ -437,18 +481,13 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                                   (acc || part > 0 || kk > 0) ? 1u : 0u);
                 commit(on, bar(kBarO + X));
             };
-            bool ok = wait(kBarQ, 0);
+            bool ok = __all_sync(kFull, mbar_wait(bar(kBarQ), 0, abort, p.wait_ns)) != 0;
             if (!split) {
                 // paired units: every tile serves both; per tile kt
                 // O_0 += P_0 V, S_0 of tile kt + 2, O_1 += P_1 V, S_1 of tile kt + 2
-                auto wait_k = [&](int kt) {
-                    const bool r = wait(kBarKFull + stg(kt), pass(kt));
-                    if (r) tc_after_sync();
-                    return r;
-                };
 #pragma unroll 1
                 for (int kt = 0; ok && kt < 2 && kt < nkv; ++kt) {
-                    ok = wait_k(kt);
+                    ok = reached(target(kNone, 0, kt + 1, 0));
                     if (!ok) break;
                     issue_s(0, kt, stg(kt));
                     if (kt < U1.nkv) issue_s(1, kt, stg(kt));
@@ -457,71 +496,69 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
 #pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
                     const int st = stg(kt), sn = stg(kt + 2), b = kt & 1;
-                    const bool a1 = kt < U1.nkv, a1n = kt + 2 < U1.nkv;
-                    ok = wait(kBarVFull + st, pass(kt)) &&
-                         (kt != nkv - 1 || !need_fix || wait(kBarVFix, 0)) &&
-                         wait(kBarP + b, (kt >> 1) & 1);
+                    const bool n0 = kt + 2 < nkv, a1 = kt < U1.nkv, a1n = kt + 2 < U1.nkv;
+                    ok = reached(target(0, kt + 1, min(kt + 3, nkv), kt + 1));
                     if (!ok) break;
-                    tc_after_sync();
                     issue_pv(0, b, st, kt > 0);
+                    if (n0) issue_s(0, b, sn);
                     if (kt == nkv - 1) commit(on, bar(kBarEnd));
                     if (!a1) commit(on, bar(kBarVEmpty + st));
-                    if (kt + 2 < nkv) {
-                        ok = wait_k(kt + 2);
-                        if (!ok) break;
-                        issue_s(0, b, sn);
-                        if (!a1n) commit(on, bar(kBarKEmpty + sn));
-                    }
+                    if (n0 && !a1n) commit(on, bar(kBarKEmpty + sn));
                     if (a1) {
-                        ok = wait(kBarP + 2 + b, (kt >> 1) & 1);
+                        ok = reached(target(1, kt + 1, 0, 0));
                         if (!ok) break;
-                        tc_after_sync();
                         issue_pv(1, b, st, kt > 0);
+                        if (a1n) issue_s(1, b, sn);
                         if (kt == U1.nkv - 1) commit(on, bar(kBarEnd + 1));
                         commit(on, bar(kBarVEmpty + st));
-                        if (a1n) {
-                            issue_s(1, b, sn);
-                            commit(on, bar(kBarKEmpty + sn));
-                        }
+                        if (a1n) commit(on, bar(kBarKEmpty + sn));
                     }
                 }
             } else {
                 // a split unit: group X = kt & 1 takes tile kt into its buffer (kt >> 1) & 1
 #pragma unroll 1
                 for (int kt = 0; ok && kt < 4 && kt < nkv; ++kt) {
-                    ok = wait(kBarKFull + stg(kt), pass(kt));
+                    ok = reached(target(kNone, 0, kt + 1, 0));
                     if (!ok) break;
-                    tc_after_sync();
                     issue_s(kt & 1, kt >> 1, stg(kt));
                     commit(on, bar(kBarKEmpty + stg(kt)));
                 }
 #pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
                     const int X = kt & 1, b = (kt >> 1) & 1;
-                    ok = wait(kBarVFull + stg(kt), pass(kt)) &&
-                         (kt != nkv - 1 || !need_fix || wait(kBarVFix, 0)) &&
-                         wait(kBarP + 2 * X + b, (kt >> 2) & 1);
+                    ok = reached(target(X, (kt >> 1) + 1, min(kt + 5, nkv), kt + 1));
                     if (!ok) break;
-                    tc_after_sync();
                     issue_pv(X, b, stg(kt), kt > 1);
+                    if (kt + 4 < nkv) issue_s(X, b, stg(kt + 4));
                     if (kt + 2 >= nkv) commit(on, bar(kBarEnd + X));
                     commit(on, bar(kBarVEmpty + stg(kt)));
-                    if (kt + 4 < nkv) {
-                        ok = wait(kBarKFull + stg(kt + 4), pass(kt + 4));
-                        if (!ok) break;
-                        tc_after_sync();
-                        issue_s(X, b, stg(kt + 4));
-                        commit(on, bar(kBarKEmpty + stg(kt + 4)));
-                    }
+                    if (kt + 4 < nkv) commit(on, bar(kBarKEmpty + stg(kt + 4)));
                 }
             }
             commit(on, bar(kBarDrain));  // every product issued has finished before tensor memory is freed
             mbar_wait(bar(kBarDrain), 0, nullptr, p.wait_ns);
         }
         __syncwarp();
+    } else if (warp == kWatchWarp) {
+        // ================= the copies' mbarriers, passed on as counters
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; ok && i < nkv + 2; ++i) {  // K runs two tiles ahead of V, as it is used
+            if (i < nkv) {
+                ok = __all_sync(kFull, mbar_wait(bar(kBarKFull + stg(i)), pass(i), abort, p.wait_ns)) != 0;
+                if (ok && lane == 0) publish(smem_u32(&counters[kCntK]), i + 1);
+            }
+            if (ok && i >= 2) {
+                const int kt = i - 2;
+                ok = __all_sync(kFull, mbar_wait(bar(kBarVFull + stg(kt)), pass(kt), abort, p.wait_ns)) != 0;
+                if (ok && kt == nkv - 1 && need_fix)
+                    ok = __all_sync(kFull, mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) != 0;
+                if (ok && lane == 0) publish(smem_u32(&counters[kCntV]), kt + 1);
+            }
+        }
     } else {
         // ================= TMA copies: warp kLoadK the q rows and the K tiles,
-        // the next warp the V tiles; a lane per 64-element box
+        // warp 10 the V tiles; a lane per 64-element box
         const bool is_k = warp == kLoadK;
         const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
         uint8_t* ring = is_k ? ksm : vsm;
