@@ -55,23 +55,22 @@ using namespace tc;
 
 constexpr int kRows = 128;          // query rows per unit (tensor-core M)
 constexpr int kTok = 64;            // KV tokens per tile (N of S, K of P V)
-constexpr int kStages = 4;          // K and V ring depth
+constexpr int kStages = 4;          // ring depth: a stage holds V of tile j and K of tile j + ahead
 constexpr int kSoftWarps = 8;       // 4 per unit: a thread per row
-constexpr int kMmaWarp = 8, kLoadK = 9, kWatchWarp = 11;  // (the V tiles: warp 10)
-constexpr int kThreads = 12 * 32;
+constexpr int kMmaWarp = 8, kWatchWarp = 10;  // (the copies: warp 9)
+constexpr int kThreads = 11 * 32;
 constexpr int kTmemCols = 512;      // S_X in columns 128 X + 64 (tile & 1).., O_X from 256 + 128 X
 
 enum : int {
-    kBarQ = 0,                         // q rows landed
-    kBarKFull = 1,                     // [stage] K tile landed
-    kBarVFull = kBarKFull + kStages,   // [stage] V tile landed
-    kBarKEmpty = kBarVFull + kStages,  // [stage] every S product of the K stage finished
-    kBarVEmpty = kBarKEmpty + kStages, // [stage] every P V product of the V stage finished
-    kBarVFix = kBarVEmpty + kStages,   // the last V tile's rows past the unit's end are zeroed
-    kBarS = kBarVFix + 1,              // [unit][buffer] S ready
-    kBarO = kBarS + 4,                 // [unit] a tile's P V finished
-    kBarEnd = kBarO + 2,               // [unit] its last P V finished
-    kBarDrain = kBarEnd + 2,           // products drained
+    kBarQ = 0,                       // q rows and the first `ahead` K tiles landed
+    kBarFull = 1,                    // [stage] its V and K tile landed
+    kBarEmpty = kBarFull + kStages,  // [stage] every product of the stage finished
+    kBarStart = kBarEmpty + kStages, // the products of the first `ahead` K tiles finished
+    kBarFix = kBarStart + 1,         // the last V tile's rows past the unit's end are zeroed
+    kBarS = kBarFix + 1,             // [unit][buffer] S ready
+    kBarO = kBarS + 4,               // [unit] P V of the tile before its last finished
+    kBarEnd = kBarO + 2,             // [unit] its last P V finished
+    kBarDrain = kBarEnd + 2,         // products drained
     kNumBars = kBarDrain + 1
 };
 
@@ -80,9 +79,8 @@ enum : int {
 // and it would need four per tile):
 enum : int {
     kCntP = 0,  // [unit][softmax warp] tiles whose P is written
-    kCntK = 8,  // K tiles landed (copied on from the mbarriers by kWatchWarp)
-    kCntV = 9,  // V tiles landed, the last one's rows past the end zeroed
-    kNumCnt = 16
+    kCntF = 8,  // stages filled (copied on from the mbarriers by kWatchWarp)
+    kNumCnt = 32  // one per lane
 };
 
 struct PfMod {
@@ -148,7 +146,7 @@ __device__ __forceinline__ bool soft_sync_or(bool flag) {
     return r != 0;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
 pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmap_q,
                             const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -243,6 +241,9 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
     // a unit alone splits its K/V tiles between the two groups (even / odd
     // tiles), whose partial results are merged at the end
     const bool split = nunits == 1;
+    // S of a tile is issued two tiles of its unit ahead of its P V
+    const int ahead = split ? 4 : 2;
+    auto kstg = [&](int kt) { return (kt + kStages - ahead) % kStages; };  // ring slot of a K tile
     const bool need_fix = (U0.kv_end % kTok) != 0;  // V rows past the end must read as zeros
 
     // ---- tensor memory, barriers
@@ -274,11 +275,10 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_addr + X * 128;
         const uint32_t tO = tmem + lane_addr + 256 + X * 128;
-        const bool capped = md.pre > 0.f, biased = md.slopes != nullptr;
-        const CapCoef cap = cap_coef(capped ? md.pre : 1.f);
+        const CapCoef cap = cap_coef(kCap ? md.pre : 1.f);
         const float sl2 = p.scale_log2;
-        const float emul = biased ? 1.f : sl2;  // without a bias the scale is applied in the exponent
-        const float slope2 = biased ? __ldg(md.slopes + (int64_t)kh * p.g + row % p.g) * 1.4426950408889634f : 0.f;
+        const float emul = kBias ? 1.f : sl2;  // without a bias the scale is applied in the exponent
+        const float slope2 = kBias ? __ldg(md.slopes + (int64_t)kh * p.g + row % p.g) * 1.4426950408889634f : 0.f;
         float mref = -INFINITY, l = 0.f;  // reference maximum (log2 domain) and sum of the row
         bool failed = false;
 #pragma unroll 1
@@ -292,16 +292,67 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                 break;
             }
             tc_after_sync();
+            // Most tiles: every column attended, no row's maximum far above its
+            // reference and no score near the cap.  P is made on that assumption in one
+            // straight run, which the compiler can interleave, and stored over the scores
+            // only if it held for every row; otherwise the scores are read again below.
+            // (Rows past the unit's end may hold anything.)
+            const bool edge = tt + kTok - 1 > U.pos0 || (window > 0 && tt <= last - window);
+            bool done = false;
+            if (!edge && i > 0) {
+                float sc[kTok];
+                tc_ld64(tSb, sc);
+                const F2 sl = f2(sl2, sl2), minus1 = f2(-1.f, -1.f), one = f2(1.f, 1.f), s2 = f2(slope2, slope2);
+                const float base = kBias ? -slope2 * (float)(pos - tt) - mref : -mref;
+                const F2 base2 = f2(base, base);
+                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+                float big[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+                uint32_t h[kTok / 2], lo[kTok / 2];
+#pragma unroll
+                for (int e = 0; e < kTok / 2; ++e) {
+                    F2 v = f2(sc[2 * e], sc[2 * e + 1]);
+                    if constexpr (kCap) {  // as cap_pairs
+                        big[e & 1] = fmaxf(big[e & 1], fmaxf(fabsf(sc[2 * e]), fabsf(sc[2 * e + 1])));
+                        const F2 z = f2_mul(v, v);
+                        v = f2_mul(v, f2_fma(z, f2_fma(z, f2_fma(z, cap.c3, cap.c2), cap.c1), one));
+                    }
+                    const F2 bias = kBias ? f2_fma(s2, f2(2.f * e, 2.f * e + 1.f), base2) : base2;
+                    const float2 x = f2_get(f2_fma(v, sl, bias));
+                    top[e & 1] = fmaxf(top[e & 1], fmaxf(x.x, x.y));
+                    const float a = ex2(x.x), b = ex2(x.y);
+                    const F2 ab = f2(a, b);
+                    sum[e & 1] = f2_add(sum[e & 1], ab);
+                    h[e] = pack2<kBf16>(a, b);
+                    if constexpr (kBf16) {
+                        const float2 hf = unpack2<true>(h[e]);
+                        const float2 r = f2_get(f2_fma(f2(hf.x, hf.y), minus1, ab));
+                        lo[e] = pack2<true>(r.x, r.y);
+                    }
+                }
+                bool bad = !(fmaxf(top[0], top[1]) <= 8.f) || mref == -INFINITY;
+                if constexpr (kCap) bad = bad || !(fmaxf(big[0], big[1]) < cap.lim);
+                if (!__any_sync(kFull, bad && pos >= 0)) {
+#pragma unroll
+                    for (int c = 0; c < kTok / 2; c += 16) {
+                        tc_st16u(tSb + c, h + c);
+                        if constexpr (kBf16) tc_st16u(tSb + kTok / 2 + c, lo + c);
+                    }
+                    const float2 t = f2_get(f2_add(sum[0], sum[1]));
+                    l += t.x + t.y;
+                    done = true;
+                }
+            }
+            if (!done) {
             float sc[kTok];
             tc_ld64(tSb, sc);
-            if (capped) cap_pairs(sc, cap);
-            if (biased) {
+            if constexpr (kCap) cap_pairs(sc, cap);
+            if constexpr (kBias) {
                 const float d0 = (float)(pos - tt);
 #pragma unroll
                 for (int c = 0; c < kTok; ++c) sc[c] = fmaf(sc[c], sl2, -slope2 * fabsf(d0 - (float)c));
             }
             // tiles with a token past the first row, or at or before the last row's window
-            if (tt + kTok - 1 > U.pos0 || (window > 0 && tt <= last - window)) {
+            if (edge) {
                 const uint64_t vis = columns_below(pre - tt) |
                                      (columns_below(pos - tt + 1) & ~(window > 0 ? columns_below(pos - window + 1 - tt) : 0ull));
                 const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
@@ -323,7 +374,9 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                 mref = mx;
             }
             if (i > 0 && __any_sync(kFull, grow)) {  // rescale O, once the previous tile's product is in it
-                ok = mbar_wait(bar(kBarO + X), (i - 1) & 1, abort, p.wait_ns);
+                // (S of the next tile was issued after it; the last tile has a barrier for it)
+                ok = i + 1 < ntiles ? mbar_wait(bar(kBarS + 2 * X + (buf ^ 1)), ((i + 1) >> 1) & 1, abort, p.wait_ns)
+                                    : mbar_wait(bar(kBarO + X), 0, abort, p.wait_ns);
                 ok = __all_sync(kFull, ok);
                 if (!ok) {
                     failed = true;
@@ -363,6 +416,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             }
             const float2 s2 = f2_get(f2_add(sum[0], sum[1]));
             l += s2.x + s2.y;
+            }
             tc_wait_st();
             tc_before_sync();
             __syncwarp();
@@ -422,36 +476,6 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         // ================= tensor-core issue
         {
             const uint32_t on = elect_one();
-            // wait until every lane's counter has reached the lane's target
-            // (bounded as mbar_wait)
-            const uint32_t cnt = smem_u32(&counters[min(lane, kNumCnt - 1)]);
-            constexpr int kNone = -1;  // a counter that does not matter
-            auto reached = [&](int target) {
-                uint64_t t0 = 0;
-                for (uint32_t it = 1;; ++it) {
-                    int v;
-                    asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(cnt) : "memory");
-                    if (__all_sync(kFull, v >= target)) {
-                        __syncwarp();  // what any lane acquired, the issuing lane has
-                        tc_after_sync();
-                        return true;
-                    }
-                    if ((it & 255) == 0) {
-                        bool stop = *abort != 0;
-                        const uint64_t now = global_ns();
-                        if (t0 == 0) t0 = now;
-                        else if (now - t0 > p.wait_ns) stop = true;
-                        if (__any_sync(kFull, stop)) {
-                            if (lane == 0) *abort = 1;
-                            return false;
-                        }
-                    }
-                }
-            };
-            // this lane's target for P of unit X, K and V tiles (as counts)
-            auto target = [&](int X, int np, int nk, int nv) {
-                return lane < kCntK ? (lane >> 2 == X ? np : kNone) : lane == kCntK ? nk : lane == kCntV ? nv : kNone;
-            };
             const uint32_t id_s = tc_idesc<kBf16>(kRows, kTok, 0);
             const uint32_t id_o = tc_idesc<kBf16>(kRows, D, 1);
             const uint64_t dq0 = tc_desc(smem_u32(qsm), 16, 1024);
@@ -478,61 +502,95 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
 #pragma unroll
                     for (int kk = 0; kk < kTok / 16; ++kk)
                         mma_ts(on, d, a + part * (kTok / 2) + kk * 8, desc_add(vd, (kk * 2048) >> 4), id_o,
-                                  (acc || part > 0 || kk > 0) ? 1u : 0u);
-                commit(on, bar(kBarO + X));
+                               (acc || part > 0 || kk > 0) ? 1u : 0u);
+            };
+            // The counters are read ahead (look), before products whose issue takes
+            // longer than the load; reached waits until every lane's counter is at the
+            // lane's target (bounded as mbar_wait).
+            const uint32_t cnt = smem_u32(&counters[lane]);
+            int seen = 0;
+            auto look = [&]() {
+                asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(seen) : "r"(cnt) : "memory");
+            };
+            auto reached = [&](int target) {
+                uint64_t t0 = 0;
+                for (uint32_t it = 1;; ++it) {
+                    if (__all_sync(kFull, seen >= target)) {
+                        __syncwarp();  // what any lane acquired, the issuing lane has
+                        tc_after_sync();
+                        return true;
+                    }
+                    if ((it & 255) == 0) {
+                        bool stop = *abort != 0;
+                        const uint64_t now = global_ns();
+                        if (t0 == 0) t0 = now;
+                        else if (now - t0 > p.wait_ns) stop = true;
+                        if (__any_sync(kFull, stop)) {
+                            if (lane == 0) *abort = 1;
+                            return false;
+                        }
+                    }
+                    look();
+                }
+            };
+            // this lane's target: n tiles' P of unit X, f stages
+            auto target = [&](int X, int n, int f) {
+                return lane < kCntF ? (lane >> 2 == X ? n : -1) : lane == kCntF ? f : -1;
             };
             bool ok = __all_sync(kFull, mbar_wait(bar(kBarQ), 0, abort, p.wait_ns)) != 0;
+            if (ok) {
+                tc_after_sync();
+                const int n = min(ahead, nkv);
+#pragma unroll 1
+                for (int kt = 0; kt < n; ++kt) {
+                    if (split) {
+                        issue_s(kt & 1, kt >> 1, kstg(kt));
+                    } else {
+                        issue_s(0, kt, kstg(kt));
+                        if (kt < U1.nkv) issue_s(1, kt, kstg(kt));
+                    }
+                }
+                commit(on, bar(kBarStart));
+                look();
+            }
             if (!split) {
                 // paired units: every tile serves both; per tile kt
                 // O_0 += P_0 V, S_0 of tile kt + 2, O_1 += P_1 V, S_1 of tile kt + 2
 #pragma unroll 1
-                for (int kt = 0; ok && kt < 2 && kt < nkv; ++kt) {
-                    ok = reached(target(kNone, 0, kt + 1, 0));
-                    if (!ok) break;
-                    issue_s(0, kt, stg(kt));
-                    if (kt < U1.nkv) issue_s(1, kt, stg(kt));
-                    commit(on, bar(kBarKEmpty + stg(kt)));
-                }
-#pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
-                    const int st = stg(kt), sn = stg(kt + 2), b = kt & 1;
+                    const int st = stg(kt), b = kt & 1;
                     const bool n0 = kt + 2 < nkv, a1 = kt < U1.nkv, a1n = kt + 2 < U1.nkv;
-                    ok = reached(target(0, kt + 1, min(kt + 3, nkv), kt + 1));
+                    ok = reached(target(0, kt + 1, kt + 1));
                     if (!ok) break;
                     issue_pv(0, b, st, kt > 0);
-                    if (n0) issue_s(0, b, sn);
+                    if (kt == nkv - 2) commit(on, bar(kBarO));
                     if (kt == nkv - 1) commit(on, bar(kBarEnd));
-                    if (!a1) commit(on, bar(kBarVEmpty + st));
-                    if (n0 && !a1n) commit(on, bar(kBarKEmpty + sn));
+                    look();
+                    if (n0) issue_s(0, b, st);
                     if (a1) {
-                        ok = reached(target(1, kt + 1, 0, 0));
+                        ok = reached(target(1, kt + 1, 0));
                         if (!ok) break;
                         issue_pv(1, b, st, kt > 0);
-                        if (a1n) issue_s(1, b, sn);
+                        if (kt == U1.nkv - 2) commit(on, bar(kBarO + 1));
                         if (kt == U1.nkv - 1) commit(on, bar(kBarEnd + 1));
-                        commit(on, bar(kBarVEmpty + st));
-                        if (a1n) commit(on, bar(kBarKEmpty + sn));
+                        look();
+                        if (a1n) issue_s(1, b, st);
                     }
+                    commit(on, bar(kBarEmpty + st));
                 }
             } else {
                 // a split unit: group X = kt & 1 takes tile kt into its buffer (kt >> 1) & 1
 #pragma unroll 1
-                for (int kt = 0; ok && kt < 4 && kt < nkv; ++kt) {
-                    ok = reached(target(kNone, 0, kt + 1, 0));
-                    if (!ok) break;
-                    issue_s(kt & 1, kt >> 1, stg(kt));
-                    commit(on, bar(kBarKEmpty + stg(kt)));
-                }
-#pragma unroll 1
                 for (int kt = 0; ok && kt < nkv; ++kt) {
-                    const int X = kt & 1, b = (kt >> 1) & 1;
-                    ok = reached(target(X, (kt >> 1) + 1, min(kt + 5, nkv), kt + 1));
+                    const int X = kt & 1, b = (kt >> 1) & 1, st = stg(kt);
+                    ok = reached(target(X, (kt >> 1) + 1, kt + 1));
                     if (!ok) break;
-                    issue_pv(X, b, stg(kt), kt > 1);
-                    if (kt + 4 < nkv) issue_s(X, b, stg(kt + 4));
+                    issue_pv(X, b, st, kt > 1);
+                    if (kt + 2 < nkv && kt + 4 >= nkv) commit(on, bar(kBarO + X));
                     if (kt + 2 >= nkv) commit(on, bar(kBarEnd + X));
-                    commit(on, bar(kBarVEmpty + stg(kt)));
-                    if (kt + 4 < nkv) commit(on, bar(kBarKEmpty + stg(kt + 4)));
+                    look();
+                    if (kt + 4 < nkv) issue_s(X, b, st);
+                    commit(on, bar(kBarEmpty + st));
                 }
             }
             commit(on, bar(kBarDrain));  // every product issued has finished before tensor memory is freed
@@ -540,81 +598,82 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         }
         __syncwarp();
     } else if (warp == kWatchWarp) {
-        // ================= the copies' mbarriers, passed on as counters
+        // ================= the copies' mbarriers, passed on as a counter
         bool ok = true;
 #pragma unroll 1
-        for (int i = 0; ok && i < nkv + 2; ++i) {  // K runs two tiles ahead of V, as it is used
-            if (i < nkv) {
-                ok = __all_sync(kFull, mbar_wait(bar(kBarKFull + stg(i)), pass(i), abort, p.wait_ns)) != 0;
-                if (ok && lane == 0) publish(smem_u32(&counters[kCntK]), i + 1);
-            }
-            if (ok && i >= 2) {
-                const int kt = i - 2;
-                ok = __all_sync(kFull, mbar_wait(bar(kBarVFull + stg(kt)), pass(kt), abort, p.wait_ns)) != 0;
-                if (ok && kt == nkv - 1 && need_fix)
-                    ok = __all_sync(kFull, mbar_wait(bar(kBarVFix), 0, abort, p.wait_ns)) != 0;
-                if (ok && lane == 0) publish(smem_u32(&counters[kCntV]), kt + 1);
-            }
+        for (int j = 0; ok && j < nkv; ++j) {
+            ok = mbar_wait(bar(kBarFull + stg(j)), pass(j), abort, p.wait_ns) &&
+                 (j != nkv - 1 || !need_fix || mbar_wait(bar(kBarFix), 0, abort, p.wait_ns));
+            ok = __all_sync(kFull, ok);
+            if (ok && lane == 0) publish(smem_u32(&counters[kCntF]), j + 1);
         }
     } else {
-        // ================= TMA copies: warp kLoadK the q rows and the K tiles,
-        // warp 10 the V tiles; a lane per 64-element box
-        const bool is_k = warp == kLoadK;
+        // ================= TMA copies: the q rows, then stage by stage V of tile j
+        // (lanes 0-7) and K of tile j + ahead (lanes 8-15), a lane per 64-element box
+        const bool is_k = (lane >> 3) & 1;
         const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
-        uint8_t* ring = is_k ? ksm : vsm;
-        const int full = is_k ? kBarKFull : kBarVFull, empty = is_k ? kBarKEmpty : kBarVEmpty;
-        if (is_k && lane == 0) {
-            mbar_expect_tx(bar(kBarQ), (uint32_t)(nunits * SM::kQ));
-#pragma unroll 1
-            for (int X = 0; X < nunits; ++X) {
-                const Unit& W = X ? U1 : U0;
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb)
-                    tma_load3(smem_u32(qsm + X * SM::kQ + cb * kRows * 128), &tmap_q, cb * 64, kh * p.g, q0 + W.tok0,
-                              bar(kBarQ));
-            }
-        }
-        __syncwarp();
+        const int jb = (lane & 7) / CB, cb = (lane & 7) % CB;  // this lane's block of a tile and column block
         const int32_t* trow = p.tables + (int64_t)s * p.mbps;
         const int lg_bs = p.bs == 16 ? 4 : 5;
         const int kt_end = p.stop_tile < 0 ? nkv : min(nkv, p.stop_tile);
-        const int jb = lane / CB, cb = lane % CB;  // this lane's block of a tile and column block
-        bool ok = true;
-        int issued = 0;
-#pragma unroll 1
-        for (int kt = 0; kt < kt_end; ++kt) {
-            const int st = stg(kt);
-            const int tt = tile_token(kt), t = tt + (jb << lg_bs);
-            const bool on = jb < (kTok >> lg_bs) && t < U0.kv_end;
+        const uint32_t box_bytes = (uint32_t)p.bs * 128;
+        // whether this lane has a box of tile kt (of K or V, as is_k says)
+        auto has_box = [&](int kt, bool kind) {
+            return kind && kt < nkv && jb < (kTok >> lg_bs) && tile_token(kt) + (jb << lg_bs) < U0.kv_end;
+        };
+        auto copy = [&](int kt, int b) {
+            const int t = tile_token(kt) + (jb << lg_bs);
             int phys = (int)p.num_blocks;  // a block that no row attends: zeros from past the pool
-            if (on && (t < pre || t + p.bs > first)) {
+            if (t < pre || t + p.bs > first) {
                 phys = __ldg(trow + (t >> lg_bs));
                 if (phys < 0 || phys >= p.num_blocks) {
                     raise_error(p.err, PKV_DEVERR_BLOCK_ID);
                     phys = 0;
                 }
             }
-            const int nbox = __popc(__ballot_sync(kFull, on));
-            if (kt >= kStages) {
-                ok = mbar_wait(bar(empty + st), pass(kt - kStages), abort, p.wait_ns);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-            }
-            if (lane == 0) mbar_expect_tx(bar(full + st), (uint32_t)(nbox * p.bs * 128));
+            uint8_t* tile = is_k ? ksm + kstg(kt) * SM::kTile : vsm + stg(kt) * SM::kTile;
+            tma_load3(smem_u32(tile + cb * kTok * 128 + jb * p.bs * 128), map, cb * 64, kh, phys * p.bs, bar(b));
+        };
+        // the q rows and the first K tiles, announced together
+        const int nfirst = min(ahead, kt_end);
+        uint32_t bytes = (uint32_t)(nunits * SM::kQ);
+        for (int kt = 0; kt < nfirst; ++kt)
+            bytes += __popc(__ballot_sync(kFull, has_box(kt, lane >= 8 && lane < 16))) * box_bytes;
+        if (lane == 0) mbar_expect_tx(bar(kBarQ), bytes);
+        __syncwarp();
+        if (lane < nunits * CB) {
+            const int X = lane / CB, qc = lane % CB;
+            tma_load3(smem_u32(qsm + X * SM::kQ + qc * kRows * 128), &tmap_q, qc * 64, kh * p.g,
+                      q0 + (X ? U1.tok0 : U0.tok0), bar(kBarQ));
+        }
+        for (int kt = 0; kt < nfirst; ++kt)
+            if (has_box(kt, lane >= 8 && lane < 16)) copy(kt, kBarQ);
+        bool ok = true;
+        int issued = 0;  // stages
+#pragma unroll 1
+        for (int j = 0; j < kt_end; ++j) {
+            // the first stages whose K tile goes where one of the first was; then
+            // the stages used before
+            if (j == kStages - ahead) ok = mbar_wait(bar(kBarStart), 0, abort, p.wait_ns);
+            if (j >= kStages) ok = ok && mbar_wait(bar(kBarEmpty + stg(j)), pass(j - kStages), abort, p.wait_ns);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            const int kt = is_k ? j + ahead : j;
+            const bool on = has_box(kt, lane < 16);
+            const uint32_t n = __popc(__ballot_sync(kFull, on));
+            if (lane == 0) mbar_expect_tx(bar(kBarFull + stg(j)), n * box_bytes);
             __syncwarp();
-            if (on)
-                tma_load3(smem_u32(ring + st * SM::kTile + cb * kTok * 128 + jb * p.bs * 128), map, cb * 64, kh,
-                          phys * p.bs, bar(full + st));
+            if (on) copy(kt, kBarFull + stg(j));
             ++issued;
         }
         if (kt_end < nkv) ok = false;  // (timeout test) the other roles wait for the missing tiles
         if (!ok) {  // let the copies in flight land before the CTA ends
-            if (is_k) mbar_wait(bar(kBarQ), 0, nullptr, p.wait_ns);
-            for (int kt = max(issued - kStages, 0); kt < issued; ++kt)
-                mbar_wait(bar(full + stg(kt)), pass(kt), nullptr, p.wait_ns);
-        } else if (!is_k && need_fix) {  // zero the last V tile's rows at and past the unit's end
+            mbar_wait(bar(kBarQ), 0, nullptr, p.wait_ns);
+            for (int j = max(issued - kStages, 0); j < issued; ++j)
+                mbar_wait(bar(kBarFull + stg(j)), pass(j), nullptr, p.wait_ns);
+        } else if (need_fix) {  // zero the last V tile's rows at and past the unit's end
             const int kl = nkv - 1, st = stg(kl);
-            bool fine = mbar_wait(bar(kBarVFull + st), pass(kl), abort, p.wait_ns);
+            bool fine = mbar_wait(bar(kBarFull + st), pass(kl), abort, p.wait_ns);
             fine = __all_sync(kFull, fine);
             if (fine) {
                 const int r0 = U0.kv_end - tile_token(kl);
@@ -624,7 +683,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                     *reinterpret_cast<uint4*>(vt + tc_off(r0 + i / CH, i % CH, kTok)) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarVFix));
+                if (lane == 0) mbar_arrive(bar(kBarFix));
             }
         }
     }
@@ -638,7 +697,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
     if (tid == 0 && abort_flag) raise_error(p.err, PKV_DEVERR_TIMEOUT);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kCap, bool kBias>
 pkv_status launch(const PrefillParams& p, const PfMod& md, const void* query, const void* kc, const void* vc,
                   int64_t num_tokens, int64_t grid, cudaStream_t st) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -654,15 +713,25 @@ pkv_status launch(const PrefillParams& p, const PfMod& md, const void* query, co
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(PKV_ECUDA, "cudaGetDevice");
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(pkv_prefill_scoremod_kernel<T, D>,
+        const cudaError_t e = cudaFuncSetAttribute(pkv_prefill_scoremod_kernel<T, D, kCap, kBias>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return fail(PKV_ECUDA, "prefill smem opt-in: %s", cudaGetErrorString(e));
         configured.fetch_or(bit);
     }
-    pkv_prefill_scoremod_kernel<T, D><<<(unsigned)grid, kThreads, kSmem, st>>>(p, tq, tk, tv, md);
+    pkv_prefill_scoremod_kernel<T, D, kCap, kBias><<<(unsigned)grid, kThreads, kSmem, st>>>(p, tq, tk, tv, md);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PKV_ECUDA, "prefill launch: %s", cudaGetErrorString(e));
     return PKV_OK;
+}
+
+template <typename T, int D>
+pkv_status dispatch(const PrefillParams& p, const PfMod& md, const void* query, const void* kc, const void* vc,
+                    int64_t num_tokens, int64_t grid, cudaStream_t st) {
+    if (md.slopes)
+        return md.pre > 0.f ? launch<T, D, true, true>(p, md, query, kc, vc, num_tokens, grid, st)
+                            : launch<T, D, false, true>(p, md, query, kc, vc, num_tokens, grid, st);
+    return md.pre > 0.f ? launch<T, D, true, false>(p, md, query, kc, vc, num_tokens, grid, st)
+                        : launch<T, D, false, false>(p, md, query, kc, vc, num_tokens, grid, st);
 }
 
 }  // namespace
@@ -697,8 +766,8 @@ extern "C" pkv_status pkv_paged_prefill_scoremod(
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const int64_t T = num_query_tokens;
     if (cache_dtype == PKV_F16)
-        return head_dim == 64 ? launch<__half, 64>(p, md, query, key_cache, value_cache, T, grid, cs)
-                              : launch<__half, 128>(p, md, query, key_cache, value_cache, T, grid, cs);
-    return head_dim == 64 ? launch<__nv_bfloat16, 64>(p, md, query, key_cache, value_cache, T, grid, cs)
-                          : launch<__nv_bfloat16, 128>(p, md, query, key_cache, value_cache, T, grid, cs);
+        return head_dim == 64 ? dispatch<__half, 64>(p, md, query, key_cache, value_cache, T, grid, cs)
+                              : dispatch<__half, 128>(p, md, query, key_cache, value_cache, T, grid, cs);
+    return head_dim == 64 ? dispatch<__nv_bfloat16, 64>(p, md, query, key_cache, value_cache, T, grid, cs)
+                          : dispatch<__nv_bfloat16, 128>(p, md, query, key_cache, value_cache, T, grid, cs);
 }
