@@ -16,7 +16,8 @@ extern "C" {
 
 /*
  * pkv_testing_prefill_timeout -- arm a timeout for the NEXT pkv_paged_prefill
- * call made by the calling thread (that call disarms it, whatever it returns).
+ * or pkv_paged_prefill_scoremod call made by the calling thread (that call disarms
+ * it, whatever it returns).
  * In that call the copy lane of every CTA copies the q rows and only the
  * K/V tiles before `stop_tile` (>= 0), then stops; the other roles wait for the
  * missing tiles, their bounded waits (limit `wait_ns` nanoseconds instead of

@@ -15,13 +15,13 @@
 //     product reads it as its A operand.  Every unit has two S buffers, so the scores
 //     of the next tile are ready when a tile's P is done.  O stays in tensor memory and
 //     is rescaled only when a row's maximum passes its reference by 2^8;
-//   - warp 8 (one lane) owns tensor memory (per unit two S of 64 and an O of
+//   - warp 8 owns tensor memory (per unit two S of 64 and an O of
 //     head_dim columns) and issues, per tile, O_0 += P_0 V, S_0'' = Q_0 K''^T, O_1 += P_1 V,
 //     S_1'' = Q_1 K''^T (the tile after the next).  Products issued by one thread run in
 //     order, so S'' may overwrite the P that the product before it reads;
-//   - warps 9 and 10 copy the K and the V tiles (4-stage rings) with TMA through the
-//     block table, a lane per box; warp 11 turns the copies' mbarriers into counters,
-//     which warp 8 reads together with the softmax warps'.
+//   - warp 9 copies the K and the V tiles (4-stage rings) with TMA through the block
+//     table, a lane per box; warp 10 turns the copies' mbarriers into a counter, which
+//     warp 8 reads together with the softmax warps'.
 // A pair's tiles are those that hold its prefix and then those from its earliest
 // row's window on; the tiles between (tile kt of the walk is tile kt of the sequence
 // up to the prefix's last, kt + gap after it) are left out.  A block of a walked tile
@@ -29,10 +29,21 @@
 // fills with zeros: its table entry is not looked at.
 // A unit without a partner splits its tiles instead: group 0 takes the even tiles,
 // group 1 the odd ones, and group 0 merges the two partial results at the end.
-// Every hand-off is an mbarrier and every wait is bounded, as in prefill.cu.
+// Every hand-off is an mbarrier or a counter and every wait is bounded, as in prefill.cu.
 //
-// Bound: the tensor core by its products (with P in two parts 1.5 times the
-// algorithm's), then the softmax warps' issue slots.
+// Measured (8192 rows of 16 / 8 heads of 128, bf16, scores capped; the last chunk of
+// 2048 rows of 32 / 8 heads at 6100 with a window of 1024 and a prefix of 200): 165 us,
+// 640 TFLOP/s of the algorithm's operations, and 66 us.  The plain prefill kernel's
+// structure with these scores (two threads per row, one S buffer) took 294 and 123 us.
+// What it took: the issuing warp run uniformly with an elected lane (one lane's branch
+// made every descriptor a vector register that the instruction had to fetch: 75 cycles a
+// product) 284 -> 224 and 159 -> 99; its waits as shared-memory counters -> 181 and
+// 70; the cap, the maxima and the exponentials in one run without a branch -> 165 and
+// 66.  Bound now: the softmax warps, two per scheduler, whose instructions wait for each
+// other's results (the schedulers issue in 47 % of the cycles, the tensor core is busy
+// in 51 %, no pipe above 40 %).  Tried without gain: two threads per row (206 us: more
+// warps, but 40 % more instructions), P beside S with S released early (190 us),
+// 128-token tiles (284 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -297,9 +308,10 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             // straight run, which the compiler can interleave, and stored over the scores
             // only if it held for every row; otherwise the scores are read again below.
             // (Rows past the unit's end may hold anything.)
-            const bool edge = tt + kTok - 1 > U.pos0 || (window > 0 && tt <= last - window);
+            const bool later = tt + kTok - 1 > U.pos0;  // a token past the first row
+            const bool edge = (later || (window > 0 && tt <= last - window)) && tt + kTok > pre;
             bool done = false;
-            if (!edge && i > 0) {
+            if (!edge && i > 0 && !(kBias && later)) {  // (the run's bias is for t <= p)
                 float sc[kTok];
                 tc_ld64(tSb, sc);
                 const F2 sl = f2(sl2, sl2), minus1 = f2(-1.f, -1.f), one = f2(1.f, 1.f), s2 = f2(slope2, slope2);

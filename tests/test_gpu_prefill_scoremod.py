@@ -162,3 +162,24 @@ def test_graph_replay():
     g.replay()
     torch.cuda.synchronize()
     check(d, out, 0.1, 9.0)
+
+
+@pytest.mark.parametrize("stop_tile", [0, 1, 3])
+def test_bounded_waits_run_out_then_the_context_recovers(stop_tile):
+    """The copies stop before tile `stop_tile`: every wait for them runs out (1 ms here), the call sets
+    PKV_DEVERR_TIMEOUT, and the next call on the same SMs finds their tensor memory free and is right."""
+    mods = dict(window=300, softcap=6.0)
+    d = setup([0, 300, 1000], [200, 64, 1], 16, 8, 128, 16, BF16, 38, 300)
+    out = torch.full_like(d["q"], 55.0)
+    assert pkv.lib().pkv_testing_prefill_timeout(stop_tile, 1_000_000) == pkv.PKV_OK
+    pkv.paged_prefill_scoremod(out, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], d["qs"], 0.09, **mods)
+    assert pkv.get_device_error() == pkv.DEVERR_TIMEOUT
+    out = run(d, 0.09, **mods)
+    check(d, out, 0.09, **mods)
+
+
+def test_many_short_chunks():
+    ctx, chunks = [(13 * i) % 90 for i in range(150)], [(7 * i) % 5 for i in range(150)]
+    d = setup(ctx, chunks, 4, 2, 64, 16, F16, 39, 20)
+    out = run(d, 0.125, window=20)
+    check(d, out, 0.125, 0.0, 20)
