@@ -50,6 +50,15 @@ pkv_status launch_decode_grid(const DecodeLaunchArgs& a, const Arg& sx, cudaStre
     return PKV_OK;
 }
 
+// CTAs of the weights pass: an item each, at most kWeightCtas per CTA of the
+// persistent grid.
+inline int64_t weight_ctas(const DecodeParams& p, int grid) {
+    const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size;
+    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads * ((cap + kWeightTokens - 1) / kWeightTokens);
+    const int64_t most = (int64_t)kWeightCtas * grid;
+    return items < most ? items : most;
+}
+
 template <class C, class Arg>
 pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_t st) {
     static_assert(C::kSmemBytes + sizeof(BlockScanSmem) <= 227 * 1024, "shared memory budget");
@@ -83,9 +92,25 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_
             cfg.stream = st;
             cfg.attrs = pdl;
             cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, pkv_merge_units_kernel<typename C::q_t, C::D, C::kTT, Arg>, p, workers, sx);
+            bool with_weights = false;
+            if constexpr (Arg::kWeights) {
+                // the weights pass in the same grid while its items are few (one
+                // launch less: 8.3 against 9.7 us for 5 sequences of up to 777 tokens;
+                // for 64 of up to 8192 tokens 101 against 93 us, every CTA making its
+                // own log sums)
+                const int64_t ctas = weight_ctas(p, a.grid);
+                with_weights = ctas <= 2 * (int64_t)a.grid && p.g <= kWeightGroup;
+                if (with_weights) {
+                    cfg.gridDim = dim3((unsigned)(units + ctas));
+                    e = cudaLaunchKernelEx(&cfg, pkv_merge_weights_kernel<typename C::q_t, C::D, C::kTT>, p, workers, sx);
+                }
+            }
+            if (!with_weights)
+                e = cudaLaunchKernelEx(&cfg, pkv_merge_units_kernel<typename C::q_t, C::D, C::kTT, Arg>, p, workers, sx);
             if (e == cudaSuccess) e = cudaGetLastError();
             if (e != cudaSuccess) return fail(PKV_ECUDA, "merge launch: %s", cudaGetErrorString(e));
+            if constexpr (Arg::kWeights)
+                if (!with_weights) return launch_weights_pass(p, sx, a.grid, st);
             return PKV_OK;
         }
     }
@@ -104,6 +129,7 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_
         e = cudaLaunchKernelEx(&cfg, pkv_merge_kernel<typename C::q_t, C::D, C::kTT, Arg>, p, workers, sx);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PKV_ECUDA, "merge launch: %s", cudaGetErrorString(e));
+    if constexpr (Arg::kWeights) return launch_weights_pass(p, sx, a.grid, st);
     return PKV_OK;
 }
 

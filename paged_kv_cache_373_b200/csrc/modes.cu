@@ -6,7 +6,7 @@
 #include <cfloat>
 #include <cmath>
 
-#include "paged_attention.cuh"
+#include "attn_launch.cuh"
 #include "pkv_internal.h"
 
 namespace pkv {
@@ -24,72 +24,20 @@ pkv_status score_cap(float softcap, float* cap2, float* inv_cap2) {
 
 namespace {
 
-// ----------------------------------------------------------------------------
-// The last pass of a decode that accumulates attention weights: for every
-// (sequence, kv head) and token t < L
-//   w = sum over the group's q heads of 2^(score - lse),
-//   out[t] = in[t] + w  (t < L - 1),   out[L - 1] = w  (the step's own token).
-// One thread owns a token, so the sum has one order and nothing is atomic.
-// The items (runs of kWeightTokens tokens of a sequence and kv head) are laid
-// end to end and every CTA takes an equal share; it finds its first one while
-// the decode pass still runs.  Scores come mostly from L2, where that pass has
-// just written them: bound by their latency, so kWeightHeads heads' loads of
-// every token are in flight together.
-// ----------------------------------------------------------------------------
-constexpr int kWeightThreads = 256, kWeightPer = 2;  // tokens per thread
-constexpr int kWeightTokens = kWeightThreads * kWeightPer;
-constexpr int kWeightHeads = 4;
-
-struct WeightsOut {
-    const float* in;  // [num_seqs, num_kv_heads, len] or null (zeros)
-    float* out;
-    int64_t len;
-};
-
+// The weights pass of large batches, after their merge pass has written every lse.
 __global__ void __launch_bounds__(kWeightThreads)
-pkv_weights_kernel(const DecodeParams p, const WeightsArg a, const WeightsOut w) {
+pkv_weights_kernel(const DecodeParams p, const WeightsArg a) {
     const WaitPrimaryAtExit<true> wait_at_exit;
     const Lens<false> ln{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq * p.block_size};
     const int64_t W = total_tiles<kWeightTokens>(ln);
     const int64_t share = (W + gridDim.x - 1) / gridDim.x;
     const int64_t tb = min(W, blockIdx.x * share), te = min(W, tb + share);
     if (tb >= te) return;
-    Walk<kWeightTokens> walk;
-    walk.init(ln, tb, te);
+    Walk<kWeightTokens> w;
+    w.init(ln, tb, te);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (; !walk.done; walk.advance(ln)) {
-        const int s = walk.s, kh = walk.j, L = walk.L, t0 = walk.i * kWeightTokens + threadIdx.x;
-        if (L > w.len && walk.i == 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
-        const int n = (int)min((int64_t)L, w.len);
-        const int64_t row0 = (int64_t)s * p.num_heads + (int64_t)kh * p.g;
-        const int64_t at = ((int64_t)s * p.num_kv_heads + kh) * w.len + t0;
-        float old[kWeightPer], acc[kWeightPer];
-#pragma unroll
-        for (int k = 0; k < kWeightPer; ++k) {
-            const int t = t0 + k * kWeightThreads;
-            old[k] = w.in && t < n && t < L - 1 ? w.in[at + k * kWeightThreads] : 0.f;
-            acc[k] = 0.f;
-        }
-        for (int h0 = 0; h0 < p.g; h0 += kWeightHeads) {
-            float x[kWeightHeads][kWeightPer], lse[kWeightHeads];
-#pragma unroll
-            for (int i = 0; i < kWeightHeads; ++i) {
-                const bool on = h0 + i < p.g;
-                lse[i] = on ? a.lse[row0 + h0 + i] : 0.f;
-                const float* sc = a.scores + (row0 + h0 + i) * a.stride + t0;
-#pragma unroll
-                for (int k = 0; k < kWeightPer; ++k)
-                    x[i][k] = on && t0 + k * kWeightThreads < n ? sc[k * kWeightThreads] : -INFINITY;
-            }
-#pragma unroll
-            for (int i = 0; i < kWeightHeads; ++i)
-#pragma unroll
-                for (int k = 0; k < kWeightPer; ++k) acc[k] += ex2(x[i][k] - lse[i]);
-        }
-#pragma unroll
-        for (int k = 0; k < kWeightPer; ++k)
-            if (t0 + k * kWeightThreads < n) w.out[at + k * kWeightThreads] = old[k] + acc[k];
-    }
+    for (; !w.done; w.advance(ln))
+        weights_item(p, a, w, a.lse + (int64_t)w.s * p.num_heads + (int64_t)w.j * p.g);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -109,6 +57,23 @@ bool weights_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
 }
 
 }  // namespace
+
+pkv_status launch_weights_pass(const DecodeParams& p, const WeightsArg& a, int grid, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)weight_ctas(p, grid));
+    cfg.blockDim = dim3(kWeightThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, pkv_weights_kernel, p, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "weights launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}
+
 }  // namespace pkv
 
 using namespace pkv;
@@ -169,29 +134,14 @@ extern "C" pkv_status pkv_paged_attention_decode_weights(
     if (workspace_bytes < l.total)
         return fail(PKV_EINVAL, "workspace too small: %zu < %zu bytes", workspace_bytes, l.total);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const WeightsArg w{reinterpret_cast<float*>(ws + l.scores), reinterpret_cast<float*>(ws + l.lse), max_tokens};
+    const WeightsArg w{reinterpret_cast<float*>(ws + l.scores), reinterpret_cast<float*>(ws + l.lse), max_tokens,
+                       weights_in, weights_out, weight_len};
     DecodeLaunchArgs a{&p, grid};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (cache_dtype) {
-    case PKV_F32: st = launch_scores_f32(a, w, head_dim, s); break;
-    case PKV_F16: st = launch_scores_f16(a, w, head_dim, s); break;
-    case PKV_BF16: st = launch_scores_bf16(a, w, head_dim, s); break;
-    default: st = launch_scores_fp8(a, w, q_dtype == PKV_BF16, s); break;
+    case PKV_F32: return launch_scores_f32(a, w, head_dim, s);
+    case PKV_F16: return launch_scores_f16(a, w, head_dim, s);
+    case PKV_BF16: return launch_scores_bf16(a, w, head_dim, s);
+    default: return launch_scores_fp8(a, w, q_dtype == PKV_BF16, s);
     }
-    if (st != PKV_OK) return st;
-    // the weights pass: a programmatic dependent of the merge pass
-    const int64_t items = (int64_t)num_seqs * num_kv_heads * ((max_tokens + kWeightTokens - 1) / kWeightTokens);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, 8 * (int64_t)pkv_default_num_ctas()));
-    cfg.blockDim = dim3(kWeightThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, pkv_weights_kernel, p, w, WeightsOut{weights_in, weights_out, weight_len});
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(PKV_ECUDA, "weights launch: %s", cudaGetErrorString(e));
-    return PKV_OK;
 }

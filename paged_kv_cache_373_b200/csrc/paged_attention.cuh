@@ -111,7 +111,10 @@ struct WeightsArg {
     static constexpr bool kSuffix = false, kMod = false, kWeights = true;
     float* scores;
     float* lse;
-    int64_t stride;  // max_blocks_per_seq * block_size
+    int64_t stride;    // max_blocks_per_seq * block_size
+    const float* in;   // [num_seqs, num_kv_heads, len]: the weights so far, or null (zeros)
+    float* out;        // and with this step's added
+    int64_t len;
 };
 
 // The cascade's prefix and suffix passes side by side on disjoint SMs: of a
@@ -1498,8 +1501,8 @@ template <typename QT, int D, int TT, class Arg>
 __global__ void __launch_bounds__(256)
 pkv_merge_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
     constexpr bool kSuffix = Arg::kSuffix;
-    // the weights pass reads what the decode grid wrote: this grid may not end before it
-    const WaitPrimaryAtExit<Arg::kWeights> wait_at_exit;
+    // what follows may read what the decode grid wrote: this grid may not end before it
+    const WaitPrimaryAtExit<Arg::kWeights || Arg::kMod> wait_at_exit;
     // a following programmatic dependent (the cascade's combine pass) may be
     // scheduled now; it waits for this grid before reading
     if constexpr (kSuffix || Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1627,7 +1630,7 @@ template <typename QT, int D, int TT, class Arg>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
     constexpr bool kSuffix = Arg::kSuffix;
-    const WaitPrimaryAtExit<Arg::kWeights> wait_at_exit;
+    const WaitPrimaryAtExit<Arg::kWeights || Arg::kMod> wait_at_exit;
     // a following programmatic dependent (the cascade's combine pass) may be
     // scheduled now; it waits for this grid before reading
     if constexpr (kSuffix || Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1759,16 +1762,13 @@ pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
 // ----------------------------------------------------------------------------
 constexpr int kUnitWarps = 8, kFold = 8;
 template <typename QT, int D, int TT, class Arg>
-__global__ void __launch_bounds__(kUnitWarps * 32)
-pkv_merge_units_kernel(const DecodeParams p, int64_t workers, const Arg ax) {
-    const WaitPrimaryAtExit<Arg::kWeights> wait_at_exit;
-    if constexpr (Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+__device__ __forceinline__ void merge_unit(const DecodeParams& p, int64_t workers, const Arg& ax, int64_t unit) {
     constexpr int PER = D / 32;
     __shared__ float part_o[kUnitWarps][D];
     __shared__ float2 part_ml[kUnitWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const auto ln = make_lens<TT>(p, ax);
-    const int s = (int)(blockIdx.x / ln.units), j = (int)(blockIdx.x % ln.units);
+    const int s = (int)(unit / ln.units), j = (int)(unit % ln.units);
     int64_t W, base;
     seq_tile_base<TT>(ln, s, &W, &base);
     const int nt = ntiles_of<TT>(ln.eff(s));
@@ -1852,6 +1852,132 @@ pkv_merge_units_kernel(const DecodeParams p, int64_t workers, const Arg ax) {
         if (lane == 0) ax.lse[row0 + h] = M + log2f(ls);
 #pragma unroll
     for (int e = 0; e < PER; ++e) out[h * D + lane + 32 * e] = from_f32<QT>(ls > 0.f ? o[e] / ls : 0.f);
+}
+
+template <typename QT, int D, int TT, class Arg>
+__global__ void __launch_bounds__(kUnitWarps * 32)
+pkv_merge_units_kernel(const DecodeParams p, int64_t workers, const Arg ax) {
+    if constexpr (Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const WaitPrimaryAtExit<true> wait_at_exit;  // this grid may not end before the decode grid
+    merge_unit<QT, D, TT>(p, workers, ax, blockIdx.x);
+}
+
+// ----------------------------------------------------------------------------
+// The last pass of a decode that accumulates attention weights: for every
+// (sequence, kv head) and token t < L
+//   w = sum over the group's q heads of 2^(score - lse),
+//   out[t] = in[t] + w  (t < L - 1),   out[L - 1] = w  (the step's own token).
+// One thread owns a token, so the sum has one order and nothing is atomic.
+// The items (runs of kWeightTokens tokens of a sequence and kv head) are laid
+// end to end and every CTA takes an equal share; it finds its first one while
+// the decode pass still runs.  Scores come mostly from L2, where that pass has
+// just written them: bound by their latency, so kWeightHeads heads' loads of
+// every token are in flight together.
+// ----------------------------------------------------------------------------
+constexpr int kWeightThreads = 256, kWeightPer = 2;  // tokens per thread
+constexpr int kWeightTokens = kWeightThreads * kWeightPer;
+constexpr int kWeightHeads = 4;
+constexpr int kWeightCtas = 8;  // per SM
+
+// One item; lse of the kv head's q heads at `lse`.
+__device__ __forceinline__ void weights_item(const DecodeParams& p, const WeightsArg& a, const Walk<kWeightTokens>& w,
+                                             const float* lse) {
+    const int L = w.L, t0 = w.i * kWeightTokens + threadIdx.x;
+    if (L > a.len && w.i == 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
+    const int n = (int)min((int64_t)L, a.len);
+    const int64_t row0 = (int64_t)w.s * p.num_heads + (int64_t)w.j * p.g;
+    const int64_t at = ((int64_t)w.s * p.num_kv_heads + w.j) * a.len + t0;
+    float old[kWeightPer], acc[kWeightPer];
+#pragma unroll
+    for (int k = 0; k < kWeightPer; ++k) {
+        const int t = t0 + k * kWeightThreads;
+        old[k] = a.in && t < n && t < L - 1 ? a.in[at + k * kWeightThreads] : 0.f;
+        acc[k] = 0.f;
+    }
+    for (int h0 = 0; h0 < p.g; h0 += kWeightHeads) {
+        float x[kWeightHeads][kWeightPer], e[kWeightHeads];
+#pragma unroll
+        for (int i = 0; i < kWeightHeads; ++i) {
+            const bool on = h0 + i < p.g;
+            e[i] = on ? lse[h0 + i] : 0.f;
+            const float* sc = a.scores + (row0 + h0 + i) * a.stride + t0;
+#pragma unroll
+            for (int k = 0; k < kWeightPer; ++k)
+                x[i][k] = on && t0 + k * kWeightThreads < n ? sc[k * kWeightThreads] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < kWeightHeads; ++i)
+#pragma unroll
+            for (int k = 0; k < kWeightPer; ++k) acc[k] += ex2(x[i][k] - e[i]);
+    }
+#pragma unroll
+    for (int k = 0; k < kWeightPer; ++k)
+        if (t0 + k * kWeightThreads < n) a.out[at + k * kWeightThreads] = old[k] + acc[k];
+}
+
+// For the smallest batches both passes in one grid: its first CTAs merge the units,
+// the others add up weights and make the log sums they need from the segments'
+// (m, l) themselves, so neither waits for the other (one launch and one grid's
+// latency less).
+constexpr int kWeightGroup = 256;  // q heads per kv head that it can hold
+template <typename QT, int D, int TT>
+__global__ void __launch_bounds__(kUnitWarps * 32)
+pkv_merge_weights_kernel(const DecodeParams p, int64_t workers, const WeightsArg a) {
+    static_assert(kUnitWarps * 32 == kWeightThreads, "one block size for both parts");
+    const WaitPrimaryAtExit<true> wait_at_exit;
+    const auto ln = make_lens<TT>(p, a);
+    const int64_t units = (int64_t)p.num_seqs * ln.units;
+    if (blockIdx.x < units) {
+        merge_unit<QT, D, TT>(p, workers, a, blockIdx.x);
+        return;
+    }
+    __shared__ float lse[kWeightGroup];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Lens<false> items{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq * p.block_size};
+    const int64_t ctas = gridDim.x - units, WI = total_tiles<kWeightTokens>(items);
+    const int64_t share = (WI + ctas - 1) / ctas;
+    const int64_t tb = min(WI, (blockIdx.x - units) * share), te = min(WI, tb + share);
+    if (tb >= te) return;
+    Walk<kWeightTokens> w;
+    w.init(items, tb, te);
+    bool waited = false;
+    for (bool first = true; !w.done; first = false, w.advance(items)) {
+        if (first || w.i == 0) {  // another kv head
+            int64_t W, base;
+            seq_tile_base<TT>(ln, w.s, &W, &base);
+            const int64_t chunk = (W + workers - 1) / workers;
+            const int nt = ntiles_of<TT>(w.L);
+            if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
+            __syncthreads();  // the last item has read lse
+            for (int hh = warp; hh < p.g; hh += kUnitWarps) {
+                const int c = hh / kHeadsPerUnit, h = hh % kHeadsPerUnit;
+                const int64_t T0 = base + (int64_t)(w.j * p.nch + c) * nt;
+                const int64_t bf = T0 / chunk, bl = (T0 + nt - 1) / chunk;
+                if (bf == bl) {  // one worker had the whole unit
+                    if (lane == 0) lse[hh] = a.lse[(int64_t)w.s * p.num_heads + (int64_t)w.j * p.g + hh];
+                    continue;
+                }
+                const int64_t u = ((int64_t)w.s * p.num_kv_heads + w.j) * p.nch + c;
+                float M = -INFINITY, l = 0.f;
+                for (int64_t k = bf + lane; k <= bl; k += 32) {
+                    const float2 ml = p.ws_ml[(k + u) * p.hpu + h];
+                    const float m = fmaxf(M, ml.x);
+                    l = l * ex2(M - m) + ml.y * ex2(ml.x - m);
+                    M = m;
+                }
+                float m = M;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                l = M == -INFINITY ? 0.f : l * ex2(M - m);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+                if (lane == 0) lse[hh] = m + log2f(l);
+            }
+            __syncthreads();
+        }
+        weights_item(p, a, w, lse);
+    }
 }
 
 }  // namespace pkv

@@ -85,6 +85,9 @@ pkv_status launch_scores_f16(const DecodeLaunchArgs&, const WeightsArg&, int hea
 pkv_status launch_scores_bf16(const DecodeLaunchArgs&, const WeightsArg&, int head_dim, cudaStream_t);
 pkv_status launch_scores_fp8(const DecodeLaunchArgs&, const WeightsArg&, bool q_bf16, cudaStream_t);
 
+// The weights pass by itself, a programmatic dependent of the merge pass (modes.cu).
+pkv_status launch_weights_pass(const DecodeParams& p, const WeightsArg& a, int grid, cudaStream_t st);
+
 // The cap of modified scores in the log2 domain (cap2 = 0: none); PKV_EINVAL
 // for a cap that is negative, not finite or too small for fp32 arithmetic.
 pkv_status score_cap(float softcap, float* cap2, float* inv_cap2);
