@@ -50,11 +50,11 @@ pkv_status launch_decode_grid(const DecodeLaunchArgs& a, const Arg& sx, cudaStre
     return PKV_OK;
 }
 
-// CTAs of the weights pass: an item each, at most kWeightCtas per CTA of the
-// persistent grid.
-inline int64_t weight_ctas(const DecodeParams& p, int grid) {
+// CTAs of the weights pass: an item each (4 tokens per thread), at most
+// kWeightCtas per CTA of the persistent grid.
+inline int64_t weight_ctas(const DecodeParams& p, int grid, int threads) {
     const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size;
-    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads * ((cap + kWeightTokens - 1) / kWeightTokens);
+    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads * ((cap + 4 * threads - 1) / (4 * threads));
     const int64_t most = (int64_t)kWeightCtas * grid;
     return items < most ? items : most;
 }
@@ -98,7 +98,7 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_
                 // launch less: 8.3 against 9.7 us for 5 sequences of up to 777 tokens;
                 // for 64 of up to 8192 tokens 101 against 93 us, every CTA making its
                 // own log sums)
-                const int64_t ctas = weight_ctas(p, a.grid);
+                const int64_t ctas = weight_ctas(p, a.grid, kUnitWarps * 32);
                 with_weights = ctas <= 2 * (int64_t)a.grid && p.g <= kWeightGroup;
                 if (with_weights) {
                     cfg.gridDim = dim3((unsigned)(units + ctas));

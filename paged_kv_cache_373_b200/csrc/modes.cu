@@ -29,15 +29,16 @@ __global__ void __launch_bounds__(kWeightThreads)
 pkv_weights_kernel(const DecodeParams p, const WeightsArg a) {
     const WaitPrimaryAtExit<true> wait_at_exit;
     const Lens<false> ln{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq * p.block_size};
-    const int64_t W = total_tiles<kWeightTokens>(ln);
+    constexpr int kTokens = kWeightThreads * 4;
+    const int64_t W = total_tiles<kTokens>(ln);
     const int64_t share = (W + gridDim.x - 1) / gridDim.x;
     const int64_t tb = min(W, blockIdx.x * share), te = min(W, tb + share);
     if (tb >= te) return;
-    Walk<kWeightTokens> w;
+    Walk<kTokens> w;
     w.init(ln, tb, te);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (; !w.done; w.advance(ln))
-        weights_item(p, a, w, a.lse + (int64_t)w.s * p.num_heads + (int64_t)w.j * p.g);
+        weights_item<kWeightThreads>(p, a, w, a.lse + (int64_t)w.s * p.num_heads + (int64_t)w.j * p.g);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -60,7 +61,7 @@ bool weights_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
 
 pkv_status launch_weights_pass(const DecodeParams& p, const WeightsArg& a, int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)weight_ctas(p, grid));
+    cfg.gridDim = dim3((unsigned)weight_ctas(p, grid, kWeightThreads));
     cfg.blockDim = dim3(kWeightThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -135,7 +136,8 @@ extern "C" pkv_status pkv_paged_attention_decode_weights(
         return fail(PKV_EINVAL, "workspace too small: %zu < %zu bytes", workspace_bytes, l.total);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const WeightsArg w{reinterpret_cast<float*>(ws + l.scores), reinterpret_cast<float*>(ws + l.lse), max_tokens,
-                       weights_in, weights_out, weight_len};
+                       weights_in, weights_out, weight_len,
+                       weight_len % 4 == 0 && aligned16(weights_in) && aligned16(weights_out)};
     DecodeLaunchArgs a{&p, grid};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (cache_dtype) {

@@ -115,6 +115,7 @@ struct WeightsArg {
     const float* in;   // [num_seqs, num_kv_heads, len]: the weights so far, or null (zeros)
     float* out;        // and with this step's added
     int64_t len;
+    bool vec;          // in and out rows are 16-byte aligned
 };
 
 // The cascade's prefix and suffix passes side by side on disjoint SMs: of a
@@ -1868,51 +1869,63 @@ pkv_merge_units_kernel(const DecodeParams p, int64_t workers, const Arg ax) {
 //   w = sum over the group's q heads of 2^(score - lse),
 //   out[t] = in[t] + w  (t < L - 1),   out[L - 1] = w  (the step's own token).
 // One thread owns a token, so the sum has one order and nothing is atomic.
-// The items (runs of kWeightTokens tokens of a sequence and kv head) are laid
+// The items (runs of 4 tokens per thread of a sequence and kv head) are laid
 // end to end and every CTA takes an equal share; it finds its first one while
 // the decode pass still runs.  Scores come mostly from L2, where that pass has
-// just written them: bound by their latency, so kWeightHeads heads' loads of
-// every token are in flight together.
+// just written them: bound by their latency, so a thread reads 16 bytes at a time
+// and has kWeightHeads heads' loads in flight together.
 // ----------------------------------------------------------------------------
-constexpr int kWeightThreads = 256, kWeightPer = 2;  // tokens per thread
-constexpr int kWeightTokens = kWeightThreads * kWeightPer;
+constexpr int kWeightThreads = 128;
 constexpr int kWeightHeads = 4;
 constexpr int kWeightCtas = 8;  // per SM
 
-// One item; lse of the kv head's q heads at `lse`.
-__device__ __forceinline__ void weights_item(const DecodeParams& p, const WeightsArg& a, const Walk<kWeightTokens>& w,
+// One item of kThreads * 4 tokens; lse of the kv head's q heads at `lse`.
+template <int kThreads>
+__device__ __forceinline__ void weights_item(const DecodeParams& p, const WeightsArg& a, const Walk<kThreads * 4>& w,
                                              const float* lse) {
-    const int L = w.L, t0 = w.i * kWeightTokens + threadIdx.x;
+    const int L = w.L, t0 = w.i * (kThreads * 4) + threadIdx.x * 4;
     if (L > a.len && w.i == 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
     const int n = (int)min((int64_t)L, a.len);
+    if (t0 >= n) return;
     const int64_t row0 = (int64_t)w.s * p.num_heads + (int64_t)w.j * p.g;
     const int64_t at = ((int64_t)w.s * p.num_kv_heads + w.j) * a.len + t0;
-    float old[kWeightPer], acc[kWeightPer];
+    const bool vec = a.vec && t0 + 4 <= n;  // the caller's rows allow 16-byte accesses
+    float old[4] = {};
+    if (a.in) {
+        if (vec) {
+            const float4 v = *reinterpret_cast<const float4*>(a.in + at);
+            old[0] = v.x; old[1] = v.y; old[2] = v.z; old[3] = v.w;
+        } else {
 #pragma unroll
-    for (int k = 0; k < kWeightPer; ++k) {
-        const int t = t0 + k * kWeightThreads;
-        old[k] = a.in && t < n && t < L - 1 ? a.in[at + k * kWeightThreads] : 0.f;
-        acc[k] = 0.f;
+            for (int k = 0; k < 4; ++k) old[k] = t0 + k < n ? a.in[at + k] : 0.f;
+        }
     }
+    float acc[4] = {};
     for (int h0 = 0; h0 < p.g; h0 += kWeightHeads) {
-        float x[kWeightHeads][kWeightPer], e[kWeightHeads];
+        float4 x[kWeightHeads];  // a score row's end is a multiple of 16 tokens: past L it holds anything
+        float e[kWeightHeads];
 #pragma unroll
         for (int i = 0; i < kWeightHeads; ++i) {
             const bool on = h0 + i < p.g;
             e[i] = on ? lse[h0 + i] : 0.f;
-            const float* sc = a.scores + (row0 + h0 + i) * a.stride + t0;
-#pragma unroll
-            for (int k = 0; k < kWeightPer; ++k)
-                x[i][k] = on && t0 + k * kWeightThreads < n ? sc[k * kWeightThreads] : -INFINITY;
+            x[i] = on ? *reinterpret_cast<const float4*>(a.scores + (row0 + h0 + i) * a.stride + t0)
+                      : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         }
 #pragma unroll
-        for (int i = 0; i < kWeightHeads; ++i)
-#pragma unroll
-            for (int k = 0; k < kWeightPer; ++k) acc[k] += ex2(x[i][k] - e[i]);
+        for (int i = 0; i < kWeightHeads; ++i) {
+            acc[0] += ex2(x[i].x - e[i]); acc[1] += ex2(x[i].y - e[i]);
+            acc[2] += ex2(x[i].z - e[i]); acc[3] += ex2(x[i].w - e[i]);
+        }
     }
 #pragma unroll
-    for (int k = 0; k < kWeightPer; ++k)
-        if (t0 + k * kWeightThreads < n) a.out[at + k * kWeightThreads] = old[k] + acc[k];
+    for (int k = 0; k < 4; ++k) acc[k] += t0 + k < L - 1 ? old[k] : 0.f;
+    if (vec) {
+        *reinterpret_cast<float4*>(a.out + at) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (t0 + k < n) a.out[at + k] = acc[k];
+    }
 }
 
 // For the smallest batches both passes in one grid: its first CTAs merge the units,
@@ -1923,7 +1936,6 @@ constexpr int kWeightGroup = 256;  // q heads per kv head that it can hold
 template <typename QT, int D, int TT>
 __global__ void __launch_bounds__(kUnitWarps * 32)
 pkv_merge_weights_kernel(const DecodeParams p, int64_t workers, const WeightsArg a) {
-    static_assert(kUnitWarps * 32 == kWeightThreads, "one block size for both parts");
     const WaitPrimaryAtExit<true> wait_at_exit;
     const auto ln = make_lens<TT>(p, a);
     const int64_t units = (int64_t)p.num_seqs * ln.units;
@@ -1931,14 +1943,15 @@ pkv_merge_weights_kernel(const DecodeParams p, int64_t workers, const WeightsArg
         merge_unit<QT, D, TT>(p, workers, a, blockIdx.x);
         return;
     }
+    constexpr int kTokens = kUnitWarps * 32 * 4;
     __shared__ float lse[kWeightGroup];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Lens<false> items{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq * p.block_size};
-    const int64_t ctas = gridDim.x - units, WI = total_tiles<kWeightTokens>(items);
+    const int64_t ctas = gridDim.x - units, WI = total_tiles<kTokens>(items);
     const int64_t share = (WI + ctas - 1) / ctas;
     const int64_t tb = min(WI, (blockIdx.x - units) * share), te = min(WI, tb + share);
     if (tb >= te) return;
-    Walk<kWeightTokens> w;
+    Walk<kTokens> w;
     w.init(items, tb, te);
     bool waited = false;
     for (bool first = true; !w.done; first = false, w.advance(items)) {
@@ -1976,7 +1989,7 @@ pkv_merge_weights_kernel(const DecodeParams p, int64_t workers, const WeightsArg
             }
             __syncthreads();
         }
-        weights_item(p, a, w, lse);
+        weights_item<kUnitWarps * 32>(p, a, w, lse);
     }
 }
 
