@@ -5,19 +5,24 @@
 //
 // Two kernels.
 //   select: one CTA per (sequence, kv head) finds the budget's threshold on the
-//     weights' bits, then numbers the kept tokens in order by ballots and one scan.
-//     Integer work only, so the result does not depend on any order.  A row of up to
-//     kBatch weights is loaded once, stays in registers and is searched bit by bit
-//     (at most 33 counts); a longer one is read again for each of three histograms
-//     (11 + 11 + 10 bits) and once more for the numbering.  Bound: the latency of
-//     its barriers.
+//     weights' bits, then numbers the kept tokens in order by ballots and one sum over
+//     the warps.  Integer work only, so the result does not depend on any order.  A row
+//     of up to kBatch weights is loaded once, stays in registers and is searched bit by
+//     bit, by the whole CTA until few keys share the prefix and then by one warp; a
+//     longer one is read again for each of three histograms (11 + 11 + 10 bits; on a row
+//     that fits the registers they took 2.4 us more) and once more for the numbering.
+//     Bound: issue slots, 1500 instructions a warp, and the passes' barriers.
 //   gather: one CTA per destination block copies its rows, 16 bytes per thread and
-//     access, K and V of four rows in flight together.  Bound: memory -- every kept row is read
-//     and written once; a row is at least one 64-byte run.
+//     access.  The blocks that hold recent tokens alone need nothing of the selection
+//     and are copied beside it.  Bound: memory -- every kept row is read and written
+//     once; a row is at least one 64-byte run.
+// 32 sequences of 1000 to 8192 tokens, 8 kv heads of 128 x 16 bits, budget 2048, recent
+// 512: 66 us, 5460 GB/s.  Without the early blocks and the one warp it was 77.5 us.
 // The source and the destination are different blocks, so nothing is moved onto
 // rows still to be read, blocks shared with other sequences stay as they are, and
 // the copy needs no order.
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -41,13 +46,21 @@ constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeys = 16;                           // weights a thread holds
 constexpr int kBatch = kSelThreads * kKeys;         // tokens the CTA holds at once
-constexpr int kRuns = kSelWarps * kKeys;            // runs of 32 neighbouring tokens in a batch
 
 // Order-preserving map of a weight to an unsigned key; NaN is the lowest, -0 is +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
     if (w != w) return 0u;
     const uint32_t b = __float_as_uint(w + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// The weight of a key, without reading it again: a load for each kept token would wait
+// for the stores before it (the compiler cannot know that they are apart), 74 us against
+// 66 in the case above.  Only the two keys that stand for several bit patterns, NaN's
+// and zero's, read theirs.
+__device__ __forceinline__ float key_weight(uint32_t key, const float* w) {
+    if (key == 0u || key == 0x80000000u) return *w;
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
 // The attended length of sequence s that the call works on, and whether its
@@ -66,8 +79,7 @@ evict_select_kernel(const EvictParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int hist[kBins];
     __shared__ int wsum[kSelWarps];
-    __shared__ int run_gt[kRuns], run_eq[kRuns];
-    __shared__ int count[2][kSelWarps];
+    __shared__ int count[2][kSelWarps], kept_of[2][kSelWarps];
     __shared__ uint32_t sh_digit;
     __shared__ int sh_left;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -82,73 +94,153 @@ evict_select_kernel(const EvictParams p) {
     const float* w = p.weights + u * p.weight_len;
     float* nw = p.new_weights + u * p.new_weight_len;
     int32_t* kept = p.kept + u * p.budget;
-    auto keep = [&](int j, int t) {
+    auto keep = [&](int j, int t, float weight) {
         if (j >= p.budget) return;
         kept[j] = t;
-        if (j < p.new_weight_len) nw[j] = w[t];
+        if (j < p.new_weight_len) nw[j] = weight;
     };
     if (L <= p.budget) {  // everything stays where it is
         for (int j = tid; j < p.budget; j += kSelThreads) {
-            if (j < L) keep(j, j);
+            if (j < L) keep(j, j, w[j]);
             else kept[j] = -1;
         }
         return;
     }
     const int m = L - p.recent;       // tokens to choose from
     const int c = p.budget - p.recent;  // of which c stay (0 <= c < m)
-    for (int t = m + tid; t < L; t += kSelThreads) keep(c + t - m, t);
-    if (c == 0) return;
+    auto keep_recent = [&] {
+        for (int t = m + tid; t < L; t += kSelThreads) keep(c + t - m, t, w[t]);
+    };
+    if (c == 0) {
+        keep_recent();
+        return;
+    }
 
     // the weights of a batch, all loads in flight; a row that fits one batch is
-    // loaded once and stays in registers through the passes
+    // loaded once and stays in registers through the passes.  A warp holds `per` runs
+    // of 32 tokens, one behind the other, so that the order of the kept tokens
+    // needs no sums across warps but one.
+    const bool one = m <= kBatch;
+    const int per = one ? (m + kSelThreads - 1) / kSelThreads : kKeys;
+    const int t0 = warp * per * 32 + lane;  // the thread's first token, from the batch's
     uint32_t key[kKeys];
-    auto load = [&](int base) {
+    auto load = [&](int base, auto meanwhile) {
         float x[kKeys];
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            if (base + i * kSelThreads >= m) break;  // (the same for every thread, here and below)
-            const int t = base + i * kSelThreads + tid;
+            if (i >= per) break;  // (the same for every thread, here and below)
+            const int t = base + t0 + 32 * i;
             x[i] = t < m ? w[t] : 0.f;
         }
+        meanwhile();
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            if (base + i * kSelThreads >= m) break;
-            key[i] = base + i * kSelThreads + tid < m ? weight_key(x[i]) : 0u;  // 0: below every candidate
+            if (i >= per) break;
+            key[i] = base + t0 + 32 * i < m ? weight_key(x[i]) : 0u;  // 0: below every candidate
         }
     };
-    const bool one = m <= kBatch;
-    if (one) load(0);
+    auto nothing = [] {};
+    if (one) load(0, keep_recent);
+    else keep_recent();
 
-    // ---- the c-th largest key.  A row in registers: bit by bit from the top, by
-    // counting the keys not below a candidate; done early when exactly c are.  A
-    // longer row: three digits by histograms, one reading of the row each.
+    // ---- the c-th largest key.  A row in registers: bit by bit from the highest bit in
+    // which its keys differ, by counting the keys not below a candidate, until exactly c
+    // are; once kSelThreads keys or fewer share the prefix those go on alone, in one
+    // warp.  A longer row: three digits by histograms, one reading of the row each.
     uint32_t prefix = 0;
     int left = c;  // rank still to find among the keys that share the prefix
     if (one) {
-        auto at_least = [&](uint32_t cand, int buf) {  // cand > 0: keys past the row are 0
+        uint32_t all = ~0u, any = 0u;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            if (i >= per) break;
+            any |= key[i];
+            if (t0 + 32 * i < m) all &= key[i];
+        }
+        all = __reduce_and_sync(kFull, all);
+        any = __reduce_or_sync(kFull, any);
+        if (lane == 0) {
+            count[0][warp] = (int)all;
+            count[1][warp] = (int)any;
+        }
+        if (tid == 0) sh_left = 0;
+        __syncthreads();
+        all = __reduce_and_sync(kFull, lane < kSelWarps ? (uint32_t)count[0][lane] : ~0u);
+        any = __reduce_or_sync(kFull, lane < kSelWarps ? (uint32_t)count[1][lane] : 0u);
+        __syncthreads();
+        int bit = 31 - __clz(all ^ any);  // -1: all keys are equal
+        prefix = bit < 0 ? all : all & ~((2u << bit) - 1);
+        int lo = m, hi = 0;  // keys not below the prefix; keys above those that share it
+        bool exact = false;
+        for (; bit >= 0 && !exact && lo - hi > kSelThreads; --bit) {
+            const uint32_t cand = prefix | (1u << bit);
             int n = 0;
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) {
-                if (i * kSelThreads >= m) break;
+                if (i >= per) break;
                 n += key[i] >= cand;
             }
             n = __reduce_add_sync(kFull, n);
-            if (lane == 0) count[buf][warp] = n;
+            if (lane == 0) count[bit & 1][warp] = n;
             __syncthreads();
-            return __reduce_add_sync(kFull, lane < kSelWarps ? count[buf][lane] : 0);
-        };
-        bool exact = false;
-        for (int b = 31; b >= 0 && !exact; --b) {
-            const uint32_t cand = prefix | (1u << b);
-            const int n = at_least(cand, b & 1);
-            if (n >= c) prefix = cand;
+            n = __reduce_add_sync(kFull, lane < kSelWarps ? count[bit & 1][lane] : 0);
+            if (n >= c) prefix = cand, lo = n;
+            else hi = n;
             exact = n == c;
         }
-        if (exact) {
-            prefix -= 1;  // the c keys not below the candidate
-            left = 0;
+        if (bit >= 0 && !exact) {
+            const uint32_t low = (2u << bit) - 1;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                if (i >= per) break;
+                const bool in = t0 + 32 * i < m && (key[i] ^ prefix) <= low;
+                const unsigned who = __ballot_sync(kFull, in);
+                if (who == 0) continue;
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&sh_left, __popc(who));  // (their order is of no matter)
+                at = __shfl_sync(kFull, at, 0) + __popc(who & ((1u << lane) - 1));
+                if (in && at < kBins) hist[at] = (int)key[i];
+            }
+            __syncthreads();
+            if (warp == 0) {
+                constexpr int kOwn = kSelThreads / 32;
+                const int own = (lo - hi + 31) / 32;  // keys a lane has (<= kOwn)
+                uint32_t mine[kOwn];
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) mine[i] = 32 * i + lane < lo - hi ? (uint32_t)hist[32 * i + lane] : 0u;
+                auto at_least = [&](uint32_t cand) {  // cand > 0
+                    int n = 0;
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i) {
+                        if (i >= own) break;
+                        n += mine[i] >= cand;
+                    }
+                    return (int)__reduce_add_sync(kFull, n);
+                };
+                left = c - hi;
+                for (; bit >= 0 && !exact; --bit) {
+                    const uint32_t cand = prefix | (1u << bit);
+                    const int n = at_least(cand);
+                    if (n >= left) prefix = cand;
+                    exact = n == left;
+                }
+                if (exact) prefix -= 1, left = 0;  // the keys not below the last candidate
+                else left -= at_least(prefix + 1);
+                if (lane == 0) {
+                    sh_digit = prefix;
+                    sh_left = left;
+                }
+            }
+            __syncthreads();
+            prefix = sh_digit;
+            left = sh_left;
+            exact = false;
         } else {
-            left = c - at_least(prefix + 1, 1);
+            left = c - hi;
+        }
+        if (exact) {
+            prefix -= 1;  // the c keys not below the last candidate
+            left = 0;
         }
     } else {
         constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
@@ -158,12 +250,11 @@ evict_select_kernel(const EvictParams p) {
             __syncthreads();
             const uint32_t mask = d == 0 ? 0u : 0xffffffffu << (kShift[d] + kBits[d]);
             for (int base = 0; base < m; base += kBatch) {
-                load(base);
+                load(base, nothing);
 #pragma unroll
                 for (int i = 0; i < kKeys; ++i) {
-                    if (base + i * kSelThreads >= m) break;
                     const uint32_t k = key[i];
-                    if (base + i * kSelThreads + tid < m && (k & mask) == prefix)
+                    if (base + t0 + 32 * i < m && (k & mask) == prefix)
                         atomicAdd(&hist[(k >> kShift[d]) & ((1u << kBits[d]) - 1)], 1);
                 }
             }
@@ -201,69 +292,59 @@ evict_select_kernel(const EvictParams p) {
     }
     // every key above `prefix` stays, and the first `left` of those equal to it
 
-    // ---- number the kept tokens in order: the ballots of a batch's runs of 32
-    // tokens (run i * kSelWarps + warp), a scan over the runs, and the totals so far
-    int gt0 = 0, eq0 = 0;
+    // ---- number the kept tokens in order: the ballots of a warp's runs, one sum over
+    // the warps, and the totals of the batches before.  `ties` false: left is 0, no
+    // token is kept for its equal key, which halves the work.
     const unsigned below = (1u << lane) - 1;
-    for (int base = 0; base < m; base += kBatch) {
-        if (!one) load(base);
+    auto number = [&](auto ties) {
+        constexpr bool kTies = decltype(ties)::value;
+        int gt0 = 0, eq0 = 0;
+        for (int base = 0; base < m; base += kBatch) {
+            if (!one) load(base, nothing);
+            auto equal = [&](int i) {
+                return kTies ? __ballot_sync(kFull, base + t0 + 32 * i < m && key[i] == prefix) : 0u;
+            };
+            unsigned above[kKeys];
+            int ng = 0, ne = 0;
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) {
-            unsigned bg = 0, be = 0;
-            if (base + i * kSelThreads < m) {
-                const bool in = base + i * kSelThreads + tid < m;
-                bg = __ballot_sync(kFull, in && key[i] > prefix);
-                be = __ballot_sync(kFull, in && key[i] == prefix);
+            for (int i = 0; i < kKeys; ++i) {
+                if (i >= per) break;
+                above[i] = __ballot_sync(kFull, key[i] > prefix);  // (a key past the row is 0)
+                ng += __popc(above[i]);
+                ne += __popc(equal(i));
             }
             if (lane == 0) {
-                run_gt[i * kSelWarps + warp] = __popc(bg);
-                run_eq[i * kSelWarps + warp] = __popc(be);
+                kept_of[0][warp] = ng;
+                kept_of[1][warp] = ne;
             }
+            __syncthreads();
+            const int vg = lane < kSelWarps ? kept_of[0][lane] : 0, ve = kTies && lane < kSelWarps ? kept_of[1][lane] : 0;
+            int g = gt0 + __reduce_add_sync(kFull, lane < warp ? vg : 0);
+            int e = kTies ? eq0 + (int)__reduce_add_sync(kFull, lane < warp ? ve : 0) : 0;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                if (i >= per) break;
+                const unsigned be = equal(i);
+                const bool is_eq = be >> lane & 1;
+                const int rank = e + __popc(be & below);
+                if (key[i] > prefix || (is_eq && rank < left))
+                    keep(g + __popc(above[i] & below) + min(rank, left), base + t0 + 32 * i, key_weight(key[i], w + base + t0 + 32 * i));
+                g += __popc(above[i]);
+                e += __popc(be);
+            }
+            if (one) break;
+            gt0 += __reduce_add_sync(kFull, vg);
+            if (kTies) eq0 += __reduce_add_sync(kFull, ve);
+            __syncthreads();
         }
-        __syncthreads();
-        if (warp < 2) {  // exclusive scan of kRuns counts, kOwn per lane; warp 0: gt, warp 1: eq
-            constexpr int kOwn = kRuns / 32;
-            static_assert(kOwn * 32 == kRuns, "every run has its lane");
-            int* run = (warp ? run_eq : run_gt) + lane * kOwn;
-            int v[kOwn], sum = 0;
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                v[i] = run[i];
-                sum += v[i];
-            }
-            int x = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lane == 31) wsum[warp] = x;
-            x -= sum;
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                run[i] = x;
-                x += v[i];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) {
-            if (base + i * kSelThreads >= m) break;
-            const int t = base + i * kSelThreads + tid;
-            const bool is_gt = t < m && key[i] > prefix, is_eq = t < m && key[i] == prefix;
-            const unsigned bg = __ballot_sync(kFull, is_gt), be = __ballot_sync(kFull, is_eq);
-            const int g = gt0 + run_gt[i * kSelWarps + warp] + __popc(bg & below);
-            const int e = eq0 + run_eq[i * kSelWarps + warp] + __popc(be & below);
-            if (is_gt || (is_eq && e < left)) keep(g + min(e, left), t);
-        }
-        gt0 += wsum[0];
-        eq0 += wsum[1];
-        __syncthreads();
-    }
+    };
+    if (left == 0) number(std::false_type{});
+    else number(std::true_type{});
 }
 
-constexpr int kGatThreads = 256;
-constexpr int kGatRows = 2;  // rows a thread has in flight
+// One row per thread and turn: two in flight cost 3 us more in the case above, 256
+// threads 1 us more.
+constexpr int kGatThreads = 512;
 
 // CTA: destination block b of sequence s.  kLanes threads hold a row, 16 bytes
 // each; the CTA's rows (slot, head) are walked in the destination's order, which is
@@ -273,15 +354,20 @@ __global__ void __launch_bounds__(kGatThreads)
 evict_gather_kernel(const EvictParams p, int nblk, int lg_bs) {
     constexpr int kStep = kGatThreads / kLanes;  // rows the CTA copies side by side
     constexpr int kRowBytes = kLanes * 16;
-    const int s = (int)(blockIdx.x / nblk), b = (int)(blockIdx.x % nblk);
+    // the sequences' last blocks first
+    const int s = (int)(blockIdx.x % p.num_seqs), b = nblk - 1 - (int)(blockIdx.x / p.num_seqs);
     bool bad;
     const int L = evict_len(p, s, &bad);
+    // A block of recent tokens alone depends on nothing of the selection and goes on
+    // beside it; the grid's last CTA always waits, so that the grid ends after it.
+    const bool early = b * p.bs >= p.budget - p.recent;
+    if (early && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool on = L > p.budget;
     const int dst = on ? __ldg(p.new_tables + (int64_t)s * p.new_mbps + b) : 0;
     const int c = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
     int slot = r0 / p.hkv, h = r0 - slot * p.hkv;
     const int dslot = kStep / p.hkv, dh = kStep - dslot * p.hkv;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!on) return;
     if (dst < 0 || dst >= p.num_blocks) {
         if (threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
@@ -292,42 +378,23 @@ evict_gather_kernel(const EvictParams p, int nblk, int lg_bs) {
     const int32_t* kept = p.kept + (int64_t)s * p.hkv * p.budget + b * p.bs;
     int64_t to = ((int64_t)dst * p.bs * p.hkv + r0) * kRowBytes + 16 * c;
     while (slot < slots) {
-        int t[kGatRows], hh[kGatRows];
-        bool in[kGatRows];
-#pragma unroll
-        for (int i = 0; i < kGatRows; ++i) {
-            in[i] = slot < slots;
-            hh[i] = h;
-            t[i] = in[i] ? kept[(int64_t)h * p.budget + slot] : 0;
-            if ((unsigned)t[i] >= (unsigned)L) { t[i] = 0; in[i] = false; }
-            slot += dslot;
-            h += dh;
-            if (h >= p.hkv) { h -= p.hkv; ++slot; }
-        }
-        int src[kGatRows];
-#pragma unroll
-        for (int i = 0; i < kGatRows; ++i) src[i] = __ldg(table + (t[i] >> lg_bs));
-        uint4 k[kGatRows], v[kGatRows];
-#pragma unroll
-        for (int i = 0; i < kGatRows; ++i) {
-            if (in[i] && (src[i] < 0 || src[i] >= p.num_blocks)) {
+        const int t = early ? L - p.budget + b * p.bs + slot : kept[(int64_t)h * p.budget + slot];
+        if ((unsigned)t < (unsigned)L) {
+            const int src = __ldg(table + (t >> lg_bs));
+            if (src < 0 || src >= p.num_blocks) {
                 if (c == 0) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
-                in[i] = false;
-            }
-            if (in[i]) {
-                const int64_t from = ((((int64_t)src[i] << lg_bs) + (t[i] & (p.bs - 1))) * p.hkv + hh[i]) * kRowBytes + 16 * c;
-                k[i] = *reinterpret_cast<const uint4*>(p.kc + from);
-                v[i] = *reinterpret_cast<const uint4*>(p.vc + from);
+            } else {
+                const int64_t from = ((((int64_t)src << lg_bs) + (t & (p.bs - 1))) * p.hkv + h) * kRowBytes + 16 * c;
+                const uint4 k = *reinterpret_cast<const uint4*>(p.kc + from);
+                const uint4 v = *reinterpret_cast<const uint4*>(p.vc + from);
+                *reinterpret_cast<uint4*>(p.kc + to) = k;
+                *reinterpret_cast<uint4*>(p.vc + to) = v;
             }
         }
-#pragma unroll
-        for (int i = 0; i < kGatRows; ++i) {
-            if (in[i]) {
-                *reinterpret_cast<uint4*>(p.kc + to) = k[i];
-                *reinterpret_cast<uint4*>(p.vc + to) = v[i];
-            }
-            to += kStep * kRowBytes;
-        }
+        slot += dslot;
+        h += dh;
+        if (h >= p.hkv) { h -= p.hkv; ++slot; }
+        to += kStep * kRowBytes;
     }
 }
 
