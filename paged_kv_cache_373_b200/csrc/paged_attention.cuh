@@ -364,6 +364,55 @@ __device__ inline SeqHit find_seq(const LN& ln, int64_t P) {
     return SeqHit{ln.S, base, 0, 0};
 }
 
+// Quotient of non-negative numbers: in 32 bits where they fit, as they do for all
+// but the largest batches (a 64-bit division is a call of some hundred cycles).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// Warp-collective, at most 32 * E sequences: total_tiles and find_seq in one pass over
+// the lengths, `at(W)` being the tile to look for (at or past W: none).
+template <int TT, int E, class LN, class At>
+__device__ __forceinline__ SeqHit lane_scan(const LN& ln, At at, int64_t* W, bool* bad_len) {
+    const int lane = threadIdx.x & 31;
+    int v[E], st[E], nt[E];
+    load_lens<E>(ln, lane * E, v, st);
+    bool bad = false;
+    int64_t own = 0;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+        bad |= v[k] < 0 || v[k] > ln.cap;
+        nt[k] = ntiles_of<TT>(ln.eff_of(v[k], st[k]));
+        own += nt[k];
+    }
+    own *= ln.units;
+    int64_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    *bad_len = __any_sync(kFull, bad);
+    *W = __shfl_sync(kFull, incl, 31);
+    const int64_t P = at(*W);
+    const unsigned hit = __ballot_sync(kFull, incl > P);
+    if (!hit) return SeqHit{ln.S, *W, 0, 0};
+    const int src = __ffs(hit) - 1;
+    int64_t base = incl - own;
+    int s = lane * E, fl = v[0], fst = st[0];
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {  // (meaningful in lane src)
+        const int64_t w = (int64_t)nt[k] * ln.units;
+        if (!found) s = lane * E + k, fl = v[k], fst = st[k];
+        found = found || base + w > P;
+        if (!found) base += w;
+    }
+    return SeqHit{__shfl_sync(kFull, s, src), __shfl_sync(kFull, base, src), __shfl_sync(kFull, fl, src),
+                  __shfl_sync(kFull, fst, src)};
+}
+
 // ----------------------------------------------------------------------------
 // CTA-cooperative forms of the two scans: the CTA's threads share one pass
 // over the lengths (kScanPerLane sequences per thread and round) instead of
@@ -516,7 +565,8 @@ struct Walk : WalkOf<LN> {
     __device__ void init(const LN& ln, int64_t tb, int64_t te_) {
         init(ln, tb, te_, tb < te_ ? find_seq<TT>(ln, tb) : SeqHit{ln.S, 0, 0, 0});
     }
-    // h: the sequence holding tile tb (find_seq or block_find_seq)
+    // h: the sequence holding tile tb (find_seq, block_find_seq or lane_scan)
+    template <bool kQuot = false>
     __device__ void init(const LN& ln, int64_t tb, int64_t te_, const SeqHit& h) {
         te = te_;
         T = tb;
@@ -529,8 +579,13 @@ struct Walk : WalkOf<LN> {
         L = ln.eff_of(h.L, h.st);
         if constexpr (LN::kHasStart) this->enter(ln, h.L, h.st);
         nt = ntiles_of<TT>(L);
-        j = (int)((tb - h.base) / nt);
-        i = (int)((tb - h.base) % nt);
+        if constexpr (kQuot) {
+            j = (int)quot(tb - h.base, nt);
+            i = (int)(tb - h.base - (int64_t)j * nt);
+        } else {
+            j = (int)((tb - h.base) / nt);
+            i = (int)((tb - h.base) % nt);
+        }
         seg_i0 = i;
         prefetch_next(ln);
     }
@@ -1408,7 +1463,17 @@ pkv_decode_kernel(const DecodeParams p, const Arg sx) {
     bool bad_len = false;
     int64_t W, tb, te;
     Walk<C::kTT, LN> iw, cw;  // issue walk (runs kStages-1 tiles ahead) and compute walk
-    if constexpr (!kWideScan) {
+    if constexpr (!kWideScan && (Arg::kMod || Arg::kWeights)) {
+        auto share = [&](int64_t total) {
+            const int64_t chunk = quot(total + workers - 1, workers);
+            tb = min(total, wid * chunk);
+            te = min(total, tb + chunk);
+            return tb;
+        };
+        const SeqHit hit = p.num_seqs <= 32 ? lane_scan<C::kTT, 1>(ln, share, &W, &bad_len)
+                                            : lane_scan<C::kTT, kScanPerLane>(ln, share, &W, &bad_len);
+        if (tb < te) iw.template init<true>(ln, tb, te, hit);
+    } else if constexpr (!kWideScan) {
         W = total_tiles<C::kTT>(ln, &bad_len);
         side_by_side(W);
         const int64_t chunk = (W + workers - 1) / workers;
