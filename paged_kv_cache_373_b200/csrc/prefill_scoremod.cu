@@ -21,7 +21,8 @@
 //     order, so S'' may overwrite the P that the product before it reads;
 //   - warp 9 copies the K and the V tiles (4-stage rings) with TMA through the block
 //     table, a lane per box; warp 10 turns the copies' mbarriers into a counter, which
-//     warp 8 reads together with the softmax warps'.
+//     warp 8 reads together with the softmax warps', and completes the V tile that the
+//     tokens end in with zeros.
 // A pair's tiles are those that hold its prefix and then those from its earliest
 // row's window on; the tiles between (tile kt of the walk is tile kt of the sequence
 // up to the prefix's last, kt + gap after it) are left out.  A block of a walked tile
@@ -32,14 +33,15 @@
 // Every hand-off is an mbarrier or a counter and every wait is bounded, as in prefill.cu.
 //
 // Measured (8192 rows of 16 / 8 heads of 128, bf16, scores capped; the last chunk of
-// 2048 rows of 32 / 8 heads at 6100 with a window of 1024 and a prefix of 200): 165 us,
-// 640 TFLOP/s of the algorithm's operations, and 66 us.  The plain prefill kernel's
+// 2048 rows of 32 / 8 heads at 6100 with a window of 1024 and a prefix of 200): 160 us,
+// 660 TFLOP/s of the algorithm's operations (P's lo part adds half as many again), and
+// 66 to 73 us; one prompt of 8192 rows of 32 / 8 heads, capped, 800 TFLOP/s.  The plain prefill kernel's
 // structure with these scores (two threads per row, one S buffer) took 294 and 123 us.
 // What it took: the issuing warp run uniformly with an elected lane (one lane's branch
 // made every descriptor a vector register that the instruction had to fetch: 75 cycles a
 // product) 284 -> 224 and 159 -> 99; its waits as shared-memory counters -> 181 and
 // 70; the cap, the maxima and the exponentials in one run without a branch -> 165 and
-// 66.  Bound now: the softmax warps, two per scheduler, whose instructions wait for each
+// 66; the pairs in the order of their lengths -> 160.  Bound now: the softmax warps, two per scheduler, whose instructions wait for each
 // other's results (the schedulers issue in 47 % of the cycles, the tensor core is busy
 // in 51 %, no pipe above 40 %).  Tried without gain: two threads per row (206 us: more
 // warps, but 40 % more instructions), P beside S with S released early (190 us),
@@ -156,6 +158,38 @@ __device__ __forceinline__ bool soft_sync_or(bool flag) {
     return r != 0;
 }
 
+// Warp-collective, 2 to 32 sequences, one per lane: the u-th longest unit pair of all,
+// as (sequence, pair, the sequence's units); sequence -1 past the last.
+__device__ __forceinline__ int3 pair_by_length(const int32_t* qstart, const int32_t* seq_lens, int* err, int num_seqs,
+                                            int g, int64_t u) {
+    const int lane = threadIdx.x & 31;
+    int C = 0, L = 0;
+    if (lane < num_seqs) {
+        C = __ldg(qstart + lane + 1) - __ldg(qstart + lane);
+        L = __ldg(seq_lens + lane);
+        if (C < 0 && blockIdx.x == 0 && threadIdx.x < 32) raise_error(err, PKV_DEVERR_SEQ_LEN);
+    }
+    const int nrt = C > 0 ? (int)(((int64_t)C * g + kRows - 1) / kRows) : 0;
+    const int npr = (nrt + 1) >> 1;
+    // pair j ends about (top - j) pairs' tokens into the sequence (top >= npr)
+    const int step = 2 * kRows / g;
+    const int top = max((int)(((int64_t)max(L, 0) + step - 1) / step), npr);
+    if (u >= (int64_t)__reduce_add_sync(kFull, (unsigned)npr)) return make_int3(-1, 0, 0);
+    // the highest x that at least u + 1 pairs reach
+    auto reach = [&](int x) { return __reduce_add_sync(kFull, (unsigned)min(max(top - x + 1, 0), npr)); };
+    int lo = 1, hi = __reduce_max_sync(kFull, npr > 0 ? top : 1);
+    while (lo < hi) {
+        const int x = lo + (hi - lo + 1) / 2;
+        if (reach(x) > u) lo = x;
+        else hi = x - 1;
+    }
+    const int at = (int)u - (int)reach(lo + 1);  // among those that end there
+    const unsigned same = __ballot_sync(kFull, top - lo >= 0 && top - lo < npr);
+    const unsigned hit = __ballot_sync(kFull, (same >> lane & 1) && __popc(same & ((1u << lane) - 1)) == at);
+    const int s = max(__ffs(hit) - 1, 0);
+    return make_int3(s, __shfl_sync(kFull, top - lo, s), __shfl_sync(kFull, nrt, s));
+}
+
 template <typename T, int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
 pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmap_q,
@@ -181,12 +215,19 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
     auto pass = [](int kt) { return (uint32_t)((kt / kStages) & 1); };
 
     // ---- the unit pair: kv head from the block index, then pair u among all
-    // sequences' pairs (a warp-parallel scan that every warp does).  A
-    // sequence's row tiles pair from the last: (n-1, n-2), (n-3, n-4), ...
+    // sequences' pairs (found by every warp).  A sequence's row tiles pair from the
+    // last: (n-1, n-2), (n-3, n-4), ...  Of 2 to 32 sequences, one per lane, the pairs
+    // are taken in the order of their lengths, so that the grid's last CTAs are short
+    // (the 8192 rows above: 160 us, by sequence 166); else sequence by sequence.
     const int kh = (int)(blockIdx.x % p.num_kv_heads);
     const int64_t u = blockIdx.x / p.num_kv_heads;
     int s = -1, jp = 0, nrt_s = 0;
-    {
+    if (p.num_seqs > 1 && p.num_seqs <= 32) {
+        const int3 at = pair_by_length(p.qstart, p.seq_lens, p.err, p.num_seqs, p.g, u);
+        s = at.x;
+        jp = at.y;
+        nrt_s = at.z;
+    } else {
         int64_t base = 0;
         for (int s0 = 0; s0 < p.num_seqs && s < 0; s0 += 32) {
             const int si = s0 + lane;

@@ -183,3 +183,40 @@ def test_many_short_chunks():
     d = setup(ctx, chunks, 4, 2, 64, 16, F16, 39, 20)
     out = run(d, 0.125, window=20)
     check(d, out, 0.125, 0.0, 20)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(2, 2, 128, BF16), (2, 2, 64, F16), (16, 1, 128, BF16)])
+@pytest.mark.parametrize("slope", [0.001, 0.5, 8.0])
+def test_bias_over_long_contexts(Hq, Hkv, D, dtype, slope):
+    # pairs whose second unit ends tiles before the first (one head per kv head), one and two units, one tile
+    ctx, chunks = [700, 0, 1500, 0, 65], [260, 600, 129, 3, 64]
+    d = setup(ctx, chunks, Hq, Hkv, D, 16, dtype, 51)
+    slopes = (slope * torch.linspace(0.5, 1.0, Hq)).cuda()
+    out = run(d, 0.1, alibi_slopes=slopes)
+    check(d, out, 0.1, slopes=slopes)
+
+
+def test_bias_with_the_reference_moving_on_every_tile():
+    # keys shrink along the sequence: walking back, each tile's maximum passes the last one's
+    d = setup([0, 100], [250, 140], 8, 2, 128, 16, BF16, 52)
+    for s, L in enumerate(d["lens"].tolist()):
+        for t in range(L):
+            b = int(d["tables"][s, t // 16])
+            row = (d["kc"][b, t % 16].float() * (1 + (L - t) / 8)).to(BF16)
+            d["kc"][b, t % 16] = row
+            d["K"][s][t] = row.double().cpu().numpy()
+    slopes = torch.linspace(0.01, 0.1, 8).cuda()
+    out = run(d, 0.2, alibi_slopes=slopes)
+    check(d, out, 0.2, slopes=slopes)
+
+
+@pytest.mark.parametrize("S", [2, 31, 32, 33])
+def test_units_of_many_sequences(S):
+    # the pairs are ordered by length for up to 32 sequences, empty chunks among them
+    g = np.random.default_rng(S)
+    chunks = [int(c) for c in g.choice([0, 1, 5, 70, 300], S)]
+    chunks[0] = 300
+    ctx = [int(c) for c in g.choice([0, 1, 90, 400], S)]
+    d = setup(ctx, chunks, 4, 2, 64, 16, F16, 53)
+    out = run(d, 0.125, softcap=10.0)
+    check(d, out, 0.125, 10.0)
