@@ -229,6 +229,18 @@ def _caches(key_cache: torch.Tensor, value_cache: torch.Tensor, index: int):
             shape)
 
 
+def _scratch(n: int, index: int, stream) -> torch.Tensor:
+    """A call's own workspace of n bytes (at least 16: a refused call needs none).  On a stream that
+    is not the current one the allocator learns of it, so that the memory is not given out again while
+    the call runs."""
+    t = torch.empty(max(n, 16), dtype=torch.uint8, device=index)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
+        t.record_stream(stream)
+    return t
+
+
 def _launch(fn, index: int, stream, *args) -> None:
     """Call a library function with CUDA device `index` current, on `stream` (default: its current one)."""
     if stream is None:
@@ -440,7 +452,7 @@ def paged_attention_decode_scoremod(out, query, key_cache, value_cache, block_ta
     dev, (S, Hq, Hkv, D, _), o, args = _decode_args(out, query, key_cache, value_cache, block_tables, seq_lens)
     if workspace is None:
         with torch.cuda.device(dev):
-            workspace = alloc_workspace(S, Hq, Hkv, D, num_ctas, device=query.device)
+            workspace = _scratch(paged_attention_workspace_bytes(S, Hq, Hkv, D, num_ctas), dev, stream)
     _launch(lib().pkv_paged_attention_decode_scoremod, dev, stream, o, *args, float(scale), float(softcap),
             int(window), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
             _arg(prefix_lens, "prefix_lens", dev, torch.int32, (S,)), _scalar(k_scale, "k_scale", dev),
@@ -468,8 +480,7 @@ def paged_attention_decode_weights(out, weights_out, query, key_cache, value_cac
     wi = _arg(weights, "weights", dev, torch.float32, wshape)
     if workspace is None:
         with torch.cuda.device(dev):
-            n = paged_attention_weights_workspace_bytes(S, Hq, Hkv, D, cap, num_ctas)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=query.device)
+            workspace = _scratch(paged_attention_weights_workspace_bytes(S, Hq, Hkv, D, cap, num_ctas), dev, stream)
     _launch(lib().pkv_paged_attention_decode_weights, dev, stream, o, wo, wi, wshape[2], *args,
             float(scale), _scalar(k_scale, "k_scale", dev), _scalar(v_scale, "v_scale", dev),
             _arg(workspace, "workspace", dev), workspace.nbytes, int(num_ctas))

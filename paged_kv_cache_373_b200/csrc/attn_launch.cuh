@@ -95,9 +95,9 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_
             bool with_weights = false;
             if constexpr (Arg::kWeights) {
                 // the weights pass in the same grid while its items are few (one
-                // launch less: 8.3 against 9.7 us for 5 sequences of up to 777 tokens;
-                // for 64 of up to 8192 tokens 101 against 93 us, every CTA making its
-                // own log sums)
+                // launch less: 1.4 us of 9.7 for 5 sequences of up to 777 tokens; for
+                // 64 of up to 8192 tokens it took 8 us more, every CTA making its own
+                // log sums)
                 const int64_t ctas = weight_ctas(p, a.grid, kUnitWarps * 32);
                 with_weights = ctas <= 2 * (int64_t)a.grid && p.g <= kWeightGroup;
                 if (with_weights) {

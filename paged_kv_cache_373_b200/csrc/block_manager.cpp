@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstring>
 #include <deque>
+#include <exception>
 #include <string>
 #include <unordered_map>
 #include <vector>
@@ -392,9 +393,10 @@ extern "C" pkv_status pkv_bm_append_batch(pkv_block_manager* bm, const int64_t* 
 }
 
 extern "C" pkv_status pkv_bm_evict_batch(pkv_block_manager* bm, const int64_t* seq_ids, int64_t n, int64_t budget,
-                                         int32_t* new_tables, int64_t new_max_blocks, int32_t* new_lens) {
+                                         int32_t* new_tables, int64_t new_max_blocks, int32_t* new_lens) try {
     if (!bm || n < 0 || budget <= 0 || new_max_blocks <= 0 || (n > 0 && (!seq_ids || !new_tables || !new_lens)))
         return bm_fail(PKV_EINVAL, "bad argument");
+    if (n > (int64_t)bm->seqs.size()) return bm_fail(PKV_EINVAL, "%lld sequences, more than there are", (long long)n);
     const int64_t nblk = (budget - 1) / bm->bs + 1;
     std::vector<Seq*> ss(n);
     std::unordered_map<int64_t, int> seen;
@@ -411,17 +413,18 @@ extern "C" pkv_status pkv_bm_evict_batch(pkv_block_manager* bm, const int64_t* s
     if (need > bm->available())
         return bm_fail(PKV_ENOBLOCKS, "eviction needs %lld blocks, %lld available", (long long)need,
                        (long long)bm->available());
+    // every allocation before the first change
     std::vector<std::vector<int32_t>> old(n);
+    for (int64_t i = 0; i < n; ++i)
+        if ((int64_t)ss[i]->tokens.size() > budget) old[i].resize(nblk);
     for (int64_t i = 0; i < n; ++i) {
         int32_t* row = new_tables + i * new_max_blocks;
         std::fill(row, row + new_max_blocks, -1);
         Seq& s = *ss[i];
         if ((int64_t)s.tokens.size() > budget) {
-            std::vector<int32_t> fresh(nblk);
-            for (int32_t& b : fresh) b = bm->take();
-            std::copy(fresh.begin(), fresh.end(), row);
-            old[i].swap(s.table);
-            s.table.swap(fresh);
+            for (int32_t& b : old[i]) b = bm->take();
+            std::copy(old[i].begin(), old[i].end(), row);
+            old[i].swap(s.table);  // the fresh blocks in, the old ones out
             s.tokens.resize(budget);  // which tokens stay differs by head: only the count is used
             s.keys.clear();
             s.evicted = true;
@@ -431,6 +434,8 @@ extern "C" pkv_status pkv_bm_evict_batch(pkv_block_manager* bm, const int64_t* s
     for (const auto& t : old)
         for (auto b = t.rbegin(); b != t.rend(); ++b) bm->drop(*b);  // tail parked first
     return PKV_OK;
+} catch (const std::exception& e) {  // out of host memory
+    return bm_fail(PKV_EINVAL, "%s", e.what());
 }
 
 extern "C" pkv_status pkv_bm_free_sequence(pkv_block_manager* bm, int64_t seq_id) {

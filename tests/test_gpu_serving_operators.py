@@ -138,3 +138,33 @@ def test_side_streams_run_two_calls_at_once():
     assert pkv.get_device_error() == 0
     for d in ds:
         check_weights(d, d["out"], d["wo"], 0.09, d["w"])
+
+
+def test_own_workspace_of_a_call_on_a_side_stream():
+    """Without a workspace the call takes its own, which memory asked for on the current stream must not be
+    while the side stream still works."""
+    from scoremod_ref import build, cuda
+    from test_gpu_decode_weights import check as check_weights
+    lens = [5000, 3, 4000, 777]
+    d = cuda(build(lens, 2, 128, 16, torch.bfloat16, 75))
+    d["q"] = torch.randn(len(lens), 8, 128, generator=torch.Generator().manual_seed(85)).to(torch.bfloat16).cuda()
+    out, wo = torch.empty_like(d["q"]), torch.empty(len(lens), 2, max(lens), device="cuda").fill_(77.0)
+    n = pkv.paged_attention_weights_workspace_bytes(len(lens), 8, 2, 128, d["tables"].shape[1] * 16)
+    m = pkv.paged_attention_workspace_bytes(len(lens), 8, 2, 128)
+    capped = torch.empty_like(out)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        out.zero_(), capped.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):  # keep the side stream busy, so that the calls wait on it
+            a = torch.randn(4096, 4096, device="cuda")
+            for _ in range(20):
+                a = a @ a * 1e-3
+        pkv.paged_attention_decode_weights(out, wo, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], 0.09, stream=stream)
+        pkv.paged_attention_decode_scoremod(capped, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], 0.09,
+                                            window=1 << 20, stream=stream)
+        held = [torch.empty(x, dtype=torch.uint8, device="cuda").fill_(255) for x in (n, m) for _ in range(8)]
+        torch.cuda.synchronize()
+        check_weights(d, out, wo, 0.09, None)
+        check_weights(d, capped, wo, 0.09, None)
+        del held, a
