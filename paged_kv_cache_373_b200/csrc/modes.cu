@@ -40,12 +40,23 @@ pkv_weights_kernel(const DecodeParams p, const WeightsArg a) {
     const WaitPrimaryAtExit<true> wait_at_exit;
     const Lens<false> ln{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq * p.block_size};
     constexpr int kTokens = kWeightThreads * 4;
-    const int64_t W = total_tiles<kTokens>(ln);
-    const int64_t share = (W + gridDim.x - 1) / gridDim.x;
-    const int64_t tb = min(W, blockIdx.x * share), te = min(W, tb + share);
-    if (tb >= te) return;
+    int64_t W, tb, te;
     Walk<kTokens> w;
-    w.init(ln, tb, te);
+    auto share = [&](int64_t total) {
+        const int64_t each = quot(total + gridDim.x - 1, gridDim.x);
+        tb = min(total, blockIdx.x * each);
+        te = min(total, tb + each);
+        return tb;
+    };
+    if (p.num_seqs <= 32 * kScanPerLane) {
+        bool bad;  // (the decode pass has raised it)
+        const SeqHit hit = lane_scan<kTokens, kScanPerLane>(ln, share, &W, &bad);
+        w.init<true>(ln, tb, te, hit);
+    } else {
+        share(W = total_tiles<kTokens>(ln));
+        w.init(ln, tb, te);
+    }
+    if (tb >= te) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (; !w.done; w.advance(ln))
         weights_item<kWeightThreads>(p, a, w, a.lse + (int64_t)w.s * p.num_heads + (int64_t)w.j * p.g);

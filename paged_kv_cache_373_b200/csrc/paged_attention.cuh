@@ -1836,23 +1836,32 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, int64_t worker
     constexpr int PER = D / 32;
     __shared__ float part_o[kUnitWarps][D];
     __shared__ float2 part_ml[kUnitWarps];
+    __shared__ int64_t first_last[2];  // the unit's first and last worker; none if it has no tiles
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const auto ln = make_lens<TT>(p, ax);
-    const int s = (int)(unit / ln.units), j = (int)(unit % ln.units);
-    int64_t W, base;
-    seq_tile_base<TT>(ln, s, &W, &base);
-    const int nt = ntiles_of<TT>(ln.eff(s));
+    const int s = (int)quot(unit, ln.units), j = (int)(unit - (int64_t)s * ln.units);
+    if (warp == 0) {  // (by every warp the search took most of the grid's issue slots)
+        int64_t W, base;
+        if (ln.S <= 32) seq_tile_base<TT, 1>(ln, s, &W, &base);
+        else seq_tile_base<TT>(ln, s, &W, &base);
+        const int nt = ntiles_of<TT>(ln.eff(s));
+        const int64_t chunk = max(quot(W + workers - 1, workers), (int64_t)1);
+        const int64_t T0 = base + (int64_t)j * nt;
+        if (lane == 0) {
+            first_last[0] = nt == 0 ? -1 : quot(T0, chunk);
+            first_last[1] = nt == 0 ? -1 : quot(T0 + nt - 1, chunk);
+        }
+    }
     const int kh = j / p.nch, c = j % p.nch;
     const int nh = min(kHeadsPerUnit, p.g - kHeadsPerUnit * c);
     const int64_t row0 = (int64_t)s * p.num_heads + (int64_t)kh * p.g + kHeadsPerUnit * c;
     QT* out = reinterpret_cast<QT*>(p.out) + row0 * D;
-    if (nt == 0) {  // nothing to attend
+    __syncthreads();
+    const int64_t bf = first_last[0], bl = first_last[1];
+    if (bf < 0) {  // nothing to attend
         for (int i = threadIdx.x; i < nh * D; i += kUnitWarps * 32) out[i] = from_f32<QT>(0.f);
         return;
     }
-    const int64_t chunk = (W + workers - 1) / workers;
-    const int64_t T0 = base + (int64_t)j * nt;
-    const int64_t bf = T0 / chunk, bl = (T0 + nt - 1) / chunk;
     if (bf == bl) return;  // one worker had the whole unit
     const int parts = kUnitWarps / nh;
     const int h = warp % nh, part = warp / nh;
