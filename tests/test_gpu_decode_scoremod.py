@@ -160,3 +160,16 @@ def test_graph_replay_reads_its_inputs_anew():
     g.replay()
     torch.cuda.synchronize()
     check(d, out, 0.1, 9.0)
+
+
+@pytest.mark.parametrize("S", [1, 32, 33, 200, 256, 257])
+def test_batch_sizes_around_the_length_scans(S):
+    g = np.random.default_rng(S)
+    lens = [int(x) for x in g.choice([0, 0, 1, 15, 16, 17, 130, 260], S)]
+    if S == 1:
+        lens = [0]     # nothing at all to attend
+    prefixes = [int(x) for x in g.integers(-2, 40, S)]
+    d = setup(lens, 4, 2, 64, 16, F16, F16, 17, 25, prefixes)
+    pre = torch.tensor(prefixes, dtype=torch.int32).cuda()
+    out = run(d, 0.125, softcap=8.0, window=25, prefix_lens=pre)
+    check(d, out, 0.125, 8.0, 25, None, prefixes)

@@ -134,3 +134,15 @@ def test_graph_replay_accumulates():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(d["w"], want)
+
+
+@pytest.mark.parametrize("S", [1, 32, 33, 200, 256, 257])
+@pytest.mark.parametrize("Hkv", [2, 8])
+def test_batch_sizes_around_the_length_scans(S, Hkv):
+    g = np.random.default_rng(S)
+    lens = [int(x) for x in g.choice([0, 0, 1, 15, 16, 17, 130, 260], S)]
+    if S == 1:
+        lens = [0]     # nothing at all to attend
+    d = setup(lens, 2 * Hkv, Hkv, 64, 16, F16, F16, 25, extra=5)  # (rows of no weights at all are refused)
+    out, wo = run(d, 0.125)
+    check(d, out, wo, 0.125, d["w"])
