@@ -816,14 +816,24 @@ struct MmaConsumer {
             // pre-scaled by a power of two per head (exact) to stay in range.
             // Thread (gid, tig) holds d = 32*tig + 4*kk + {0,1,2,3}: the same
             // permutation of the contraction index as its K fragments.
+            // (read 16 bytes at a time: by single elements the 8 heads' rows, 256
+            // bytes apart, met in the same banks, 3 us of a small call)
             using QT = typename C::q_t;
-            const QT* qh = reinterpret_cast<const QT*>(qs) + gid * D + 32 * tig;
+            constexpr bool kQb = std::is_same<QT, __nv_bfloat16>::value;
+            const uint4* qh = reinterpret_cast<const uint4*>(qs + (gid * D + 32 * tig) * sizeof(QT));
             float v[32];
             float amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                v[i] = (gid < nh) ? static_cast<float>(qh[i]) : 0.f;
-                amax = fmaxf(amax, fabsf(v[i]));
+            for (int i = 0; i < 4; ++i) {
+                const uint4 r = gid < nh ? qh[i] : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = unpack2<kQb>(w[k]);
+                    v[8 * i + 2 * k] = f.x;
+                    v[8 * i + 2 * k + 1] = f.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
             }
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
@@ -1077,6 +1087,25 @@ struct MmaConsumer {
                         *reinterpret_cast<uint32_t*>(out + h1 * D + 16 * gid + 2 * mi) =
                             pack2<kQb>(acc[mi][1] * s1, acc[mi][3] * s1);
                 }
+            }
+            return;
+        }
+        if constexpr (kFp8 && !kPart) {
+            // a partial: the lane's 16 neighbouring d of each head, 16 bytes at a time
+            // (by single floats every store of the warp touched 32 sectors)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = e ? h1 : h0;
+                if (h >= k.nh) continue;
+                float4* dst = reinterpret_cast<float4*>(p.ws_o + (k.seg * p.hpu + h) * D + 16 * gid);
+#pragma unroll
+                for (int mi = 0; mi < MT; mi += 2)
+                    dst[mi / 2] = make_float4(acc[mi][e] * vscale, acc[mi][2 + e] * vscale,
+                                              acc[mi + 1][e] * vscale, acc[mi + 1][2 + e] * vscale);
+            }
+            if (gid == 0) {
+                if (h0 < k.nh) p.ws_ml[k.seg * p.hpu + h0] = make_float2(m0, a0);
+                if (h1 < k.nh) p.ws_ml[k.seg * p.hpu + h1] = make_float2(m1, a1);
             }
             return;
         }
