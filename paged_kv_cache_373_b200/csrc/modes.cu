@@ -6,13 +6,13 @@
 //
 // Bound: memory for large batches, the chain of dependent loads (lengths, table,
 // K and V, partial results) for small ones.  With modified scores: 128 sequences of
-// 64 to 8192 tokens, 32 / 8 heads of 128, bf16, capped: 145 us, 6060 GB/s (the K and V
-// bytes once); 3 sequences of up to 301 tokens 6.1 us; 16 FP8 sequences with a window
-// of 4096 and 64 kept tokens 40 us, 3400 GB/s, of which 25 us are the tile loop (5400
+// 64 to 8192 tokens, 32 / 8 heads of 128, bf16, capped: 141 us, 6250 GB/s (the K and V
+// bytes once); 3 sequences of up to 301 tokens 6.0 us; 16 FP8 sequences with a window
+// of 4096 and 64 kept tokens 35 us, 3900 GB/s, of which 25 us are the tile loop (5400
 // GB/s) and the rest its start and the merge.  With weights: 64 sequences of 64 to
-// 8192 tokens 87 us, 5130 GB/s: the decode pass 74, the merge 5, the weights pass 8 (its
+// 8192 tokens 86 us, 5220 GB/s: the decode pass 74, the merge 4, the weights pass 8 (its
 // scores, 4 bytes per q head and token, written once and read once, mostly in L2);
-// 5 sequences of up to 777 tokens 7.1 us.
+// 5 sequences of up to 777 tokens 7.0 us.
 #include <cfloat>
 #include <cmath>
 

@@ -1077,15 +1077,20 @@ struct MmaConsumer {
                     }
                 }
             } else {
-                // FP8 path: lane holds d = 16 gid + 2 mi and the next one of heads h0, h1
+                // FP8 path: lane holds d = 16 gid + 2 mi and the next one of heads h0, h1:
+                // 32 contiguous bytes of each
 #pragma unroll
-                for (int mi = 0; mi < MT; ++mi) {
-                    if (h0 < k.nh)
-                        *reinterpret_cast<uint32_t*>(out + h0 * D + 16 * gid + 2 * mi) =
-                            pack2<kQb>(acc[mi][0] * s0, acc[mi][2] * s0);
-                    if (h1 < k.nh)
-                        *reinterpret_cast<uint32_t*>(out + h1 * D + 16 * gid + 2 * mi) =
-                            pack2<kQb>(acc[mi][1] * s1, acc[mi][3] * s1);
+                for (int e = 0; e < 2; ++e) {
+                    const int h = e ? h1 : h0;
+                    const float sc = e ? s1 : s0;
+                    if (h >= k.nh) continue;
+                    uint4* dst = reinterpret_cast<uint4*>(out + h * D + 16 * gid);
+#pragma unroll
+                    for (int mi = 0; mi < MT; mi += 4)
+                        dst[mi / 4] = make_uint4(pack2<kQb>(acc[mi][e] * sc, acc[mi][2 + e] * sc),
+                                                 pack2<kQb>(acc[mi + 1][e] * sc, acc[mi + 1][2 + e] * sc),
+                                                 pack2<kQb>(acc[mi + 2][e] * sc, acc[mi + 2][2 + e] * sc),
+                                                 pack2<kQb>(acc[mi + 3][e] * sc, acc[mi + 3][2 + e] * sc));
                 }
             }
             return;
