@@ -54,14 +54,50 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// The weight of a key, without reading it again: a load for each kept token would wait
-// for the stores before it (the compiler cannot know that they are apart), 74 us against
-// 66 in the case above.  Only the two keys that stand for several bit patterns, NaN's
-// and zero's, read theirs.
-__device__ __forceinline__ float key_weight(uint32_t key, const float* w) {
-    if (key == 0u || key == 0x80000000u) return *w;
+// The weight of a key, but for the two keys that stand for several bit patterns, NaN's
+// and zero's.
+__device__ __forceinline__ float key_weight(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
+__device__ __forceinline__ bool key_is_exact(uint32_t key) { return key != 0u && key != 0x80000000u; }
+
+// How many of the warp's keys (n per lane, at most 16) are not below each of three
+// candidates, 10 bits each: two bits of a threshold for one reduction.
+template <int N>
+__device__ __forceinline__ uint32_t count3(const uint32_t (&key)[N], int n, uint32_t c1, uint32_t c2, uint32_t c3) {
+    static_assert(N * 32 < 1024, "10 bits");
+    uint32_t a = 0, b = 0, c = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (i >= n) break;
+        a += key[i] >= c1 ? 1u : 0u;
+        b += key[i] >= c2 ? 1u << 10 : 0u;
+        c += key[i] >= c3 ? 1u << 20 : 0u;
+    }
+    return __reduce_add_sync(kFull, a + b + c);
+}
+
+// The candidates of the next step below `bit` (the last step has one bit, and two that no
+// key reaches), and the step's result: the highest of them that at least `want` keys
+// reach becomes the prefix.  lo, hi: keys not below the prefix, and above those that
+// share it.
+struct Step {
+    int sh;
+    uint32_t c1, c2, c3;
+    __device__ __forceinline__ Step(uint32_t prefix, int bit) {
+        sh = bit > 0 ? bit - 1 : 0;
+        c1 = prefix | (1u << sh);
+        c2 = bit > 0 ? prefix | (2u << sh) : ~0u;
+        c3 = bit > 0 ? prefix | (3u << sh) : ~0u;
+    }
+    __device__ __forceinline__ void take(int n1, int n2, int n3, int want, int& bit, uint32_t& prefix, int& lo, int& hi) {
+        if (n3 >= want) prefix = c3, lo = n3;
+        else if (n2 >= want) prefix = c2, lo = n2, hi = n3;
+        else if (n1 >= want) prefix = c1, lo = n1, hi = bit > 0 ? n2 : hi;
+        else hi = n1;
+        bit = sh - 1;
+    }
+};
 
 // The attended length of sequence s that the call works on, and whether its
 // tables and rows hold it.
@@ -94,10 +130,10 @@ evict_select_kernel(const EvictParams p) {
     const float* w = p.weights + u * p.weight_len;
     float* nw = p.new_weights + u * p.new_weight_len;
     int32_t* kept = p.kept + u * p.budget;
+    const int nw_len = (int)min(p.new_weight_len, (int64_t)p.budget);
     auto keep = [&](int j, int t, float weight) {
-        if (j >= p.budget) return;
-        kept[j] = t;
-        if (j < p.new_weight_len) nw[j] = weight;
+        if (j < p.budget) kept[j] = t;
+        if (j < nw_len) nw[j] = weight;
     };
     if (L <= p.budget) {  // everything stays where it is
         for (int j = tid; j < p.budget; j += kSelThreads) {
@@ -172,21 +208,15 @@ evict_select_kernel(const EvictParams p) {
         prefix = bit < 0 ? all : all & ~((2u << bit) - 1);
         int lo = m, hi = 0;  // keys not below the prefix; keys above those that share it
         bool exact = false;
-        for (; bit >= 0 && !exact && lo - hi > kSelThreads; --bit) {
-            const uint32_t cand = prefix | (1u << bit);
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) {
-                if (i >= per) break;
-                n += key[i] >= cand;
-            }
-            n = __reduce_add_sync(kFull, n);
-            if (lane == 0) count[bit & 1][warp] = n;
+        for (int buf = 0; bit >= 0 && !exact && lo - hi > kSelThreads; buf ^= 1) {
+            Step step(prefix, bit);
+            const uint32_t mine = count3(key, per, step.c1, step.c2, step.c3);
+            if (lane == 0) count[buf][warp] = (int)mine;
             __syncthreads();
-            n = __reduce_add_sync(kFull, lane < kSelWarps ? count[bit & 1][lane] : 0);
-            if (n >= c) prefix = cand, lo = n;
-            else hi = n;
-            exact = n == c;
+            const uint32_t v = lane < kSelWarps ? (uint32_t)count[buf][lane] : 0u;
+            step.take((int)__reduce_add_sync(kFull, v & 1023u), (int)__reduce_add_sync(kFull, v >> 10 & 1023u),
+                      (int)__reduce_add_sync(kFull, v >> 20), c, bit, prefix, lo, hi);
+            exact = lo == c;
         }
         if (bit >= 0 && !exact) {
             const uint32_t low = (2u << bit) - 1;
@@ -208,24 +238,15 @@ evict_select_kernel(const EvictParams p) {
                 uint32_t mine[kOwn];
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) mine[i] = 32 * i + lane < lo - hi ? (uint32_t)hist[32 * i + lane] : 0u;
-                auto at_least = [&](uint32_t cand) {  // cand > 0
-                    int n = 0;
-#pragma unroll
-                    for (int i = 0; i < kOwn; ++i) {
-                        if (i >= own) break;
-                        n += mine[i] >= cand;
-                    }
-                    return (int)__reduce_add_sync(kFull, n);
-                };
                 left = c - hi;
-                for (; bit >= 0 && !exact; --bit) {
-                    const uint32_t cand = prefix | (1u << bit);
-                    const int n = at_least(cand);
-                    if (n >= left) prefix = cand;
-                    exact = n == left;
+                int in = lo - hi, above = 0;  // of these keys
+                while (bit >= 0 && in != left) {
+                    Step step(prefix, bit);
+                    const uint32_t v = count3(mine, own, step.c1, step.c2, step.c3);
+                    step.take((int)(v & 1023u), (int)(v >> 10 & 1023u), (int)(v >> 20), left, bit, prefix, in, above);
                 }
-                if (exact) prefix -= 1, left = 0;  // the keys not below the last candidate
-                else left -= at_least(prefix + 1);
+                if (in == left) prefix -= 1, left = 0;  // the keys not below the prefix
+                else left -= above;
                 if (lane == 0) {
                     sh_digit = prefix;
                     sh_left = left;
@@ -234,13 +255,11 @@ evict_select_kernel(const EvictParams p) {
             __syncthreads();
             prefix = sh_digit;
             left = sh_left;
-            exact = false;
-        } else {
-            left = c - hi;
-        }
-        if (exact) {
-            prefix -= 1;  // the c keys not below the last candidate
+        } else if (exact) {
+            prefix -= 1;  // the c keys not below the prefix
             left = 0;
+        } else {
+            left = c - hi;  // all keys that share the prefix are equal
         }
     } else {
         constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
@@ -321,16 +340,36 @@ evict_select_kernel(const EvictParams p) {
             const int vg = lane < kSelWarps ? kept_of[0][lane] : 0, ve = kTies && lane < kSelWarps ? kept_of[1][lane] : 0;
             int g = gt0 + __reduce_add_sync(kFull, lane < warp ? vg : 0);
             int e = kTies ? eq0 + (int)__reduce_add_sync(kFull, lane < warp ? ve : 0) : 0;
+            // The weights go out from their keys: reading each again would wait for the
+            // stores before it (the compiler cannot know that they are apart), 74 us
+            // against 66 in the case above.  The kept zeros and NaN are read afterwards.
+            uint32_t again = 0;
+            const int g_first = g, e_first = e;
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) {
                 if (i >= per) break;
                 const unsigned be = equal(i);
                 const bool is_eq = be >> lane & 1;
                 const int rank = e + __popc(be & below);
-                if (key[i] > prefix || (is_eq && rank < left))
-                    keep(g + __popc(above[i] & below) + min(rank, left), base + t0 + 32 * i, key_weight(key[i], w + base + t0 + 32 * i));
+                if (key[i] > prefix || (is_eq && rank < left)) {
+                    const int j = g + __popc(above[i] & below) + min(rank, left);
+                    keep(j, base + t0 + 32 * i, key_weight(key[i]));
+                    if (!key_is_exact(key[i])) again |= 1u << i;
+                }
                 g += __popc(above[i]);
                 e += __popc(be);
+            }
+            if (__any_sync(kFull, again != 0)) {
+                int g2 = g_first, e2 = e_first;
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) {
+                    if (i >= per) break;
+                    const unsigned be = equal(i);
+                    const int j = g2 + __popc(above[i] & below) + min(e2 + __popc(be & below), left);
+                    if ((again >> i & 1) && j < nw_len) nw[j] = w[base + t0 + 32 * i];
+                    g2 += __popc(above[i]);
+                    e2 += __popc(be);
+                }
             }
             if (one) break;
             gt0 += __reduce_add_sync(kFull, vg);
