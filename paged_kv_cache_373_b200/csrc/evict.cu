@@ -7,8 +7,8 @@
 //   select: one CTA per (sequence, kv head) finds the budget's threshold on the
 //     weights' bits, then numbers the kept tokens in order by ballots and one sum over
 //     the warps.  Integer work only, so the result does not depend on any order.  A row
-//     of up to kBatch weights is loaded once, stays in registers and is searched bit by
-//     bit, by the whole CTA until few keys share the prefix and then by one warp; a
+//     of up to kBatch weights is loaded once, stays in registers and is searched two bits
+//     at a time, by the whole CTA until few keys share the prefix and then by one warp; a
 //     longer one is read again for each of three histograms (11 + 11 + 10 bits; on a row
 //     that fits the registers they took 2.4 us more) and once more for the numbering.
 //     Bound: issue slots, 1500 instructions a warp, and the passes' barriers.
@@ -17,7 +17,9 @@
 //     and are copied beside it.  Bound: memory -- every kept row is read and written
 //     once; a row is at least one 64-byte run.
 // 32 sequences of 1000 to 8192 tokens, 8 kv heads of 128 x 16 bits, budget 2048, recent
-// 512: 66 us, 5460 GB/s.  Without the early blocks and the one warp it was 77.5 us.
+// 512: 64.5 us, 5580 GB/s.  Without the early blocks and the one warp it was 77.5 us.
+// One sequence of 8192 tokens, 8 kv heads: 18 us; of 20000 40.7 us.  1024 threads with 31
+// keys each take 29.6 us there, but 71.5 for the 32 sequences above.
 // The source and the destination are different blocks, so nothing is moved onto
 // rows still to be read, blocks shared with other sequences stay as they are, and
 // the copy needs no order.
@@ -46,6 +48,8 @@ constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeys = 16;                           // weights a thread holds
 constexpr int kBatch = kSelThreads * kKeys;         // tokens the CTA holds at once
+constexpr int kList = 512;                          // keys that one warp searches alone
+static_assert(kList <= kBins, "they lie in the histogram's memory");
 
 // Order-preserving map of a weight to an unsigned key; NaN is the lowest, -0 is +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -110,7 +114,7 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int s, bool* bad)
     return L;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 2)
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
 evict_select_kernel(const EvictParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int hist[kBins];
@@ -181,7 +185,7 @@ evict_select_kernel(const EvictParams p) {
 
     // ---- the c-th largest key.  A row in registers: bit by bit from the highest bit in
     // which its keys differ, by counting the keys not below a candidate, until exactly c
-    // are; once kSelThreads keys or fewer share the prefix those go on alone, in one
+    // are; once kList keys or fewer share the prefix those go on alone, in one
     // warp.  A longer row: three digits by histograms, one reading of the row each.
     uint32_t prefix = 0;
     int left = c;  // rank still to find among the keys that share the prefix
@@ -208,7 +212,7 @@ evict_select_kernel(const EvictParams p) {
         prefix = bit < 0 ? all : all & ~((2u << bit) - 1);
         int lo = m, hi = 0;  // keys not below the prefix; keys above those that share it
         bool exact = false;
-        for (int buf = 0; bit >= 0 && !exact && lo - hi > kSelThreads; buf ^= 1) {
+        for (int buf = 0; bit >= 0 && !exact && lo - hi > kList; buf ^= 1) {
             Step step(prefix, bit);
             const uint32_t mine = count3(key, per, step.c1, step.c2, step.c3);
             if (lane == 0) count[buf][warp] = (int)mine;
@@ -233,7 +237,7 @@ evict_select_kernel(const EvictParams p) {
             }
             __syncthreads();
             if (warp == 0) {
-                constexpr int kOwn = kSelThreads / 32;
+                constexpr int kOwn = kList / 32;
                 const int own = (lo - hi + 31) / 32;  // keys a lane has (<= kOwn)
                 uint32_t mine[kOwn];
 #pragma unroll
@@ -323,13 +327,12 @@ evict_select_kernel(const EvictParams p) {
             auto equal = [&](int i) {
                 return kTies ? __ballot_sync(kFull, base + t0 + 32 * i < m && key[i] == prefix) : 0u;
             };
-            unsigned above[kKeys];
+            auto above = [&](int i) { return __ballot_sync(kFull, key[i] > prefix); };  // (a key past the row is 0)
             int ng = 0, ne = 0;
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) {
                 if (i >= per) break;
-                above[i] = __ballot_sync(kFull, key[i] > prefix);  // (a key past the row is 0)
-                ng += __popc(above[i]);
+                ng += __popc(above(i));
                 ne += __popc(equal(i));
             }
             if (lane == 0) {
@@ -348,15 +351,15 @@ evict_select_kernel(const EvictParams p) {
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) {
                 if (i >= per) break;
-                const unsigned be = equal(i);
+                const unsigned ba = above(i), be = equal(i);
                 const bool is_eq = be >> lane & 1;
                 const int rank = e + __popc(be & below);
                 if (key[i] > prefix || (is_eq && rank < left)) {
-                    const int j = g + __popc(above[i] & below) + min(rank, left);
+                    const int j = g + __popc(ba & below) + min(rank, left);
                     keep(j, base + t0 + 32 * i, key_weight(key[i]));
                     if (!key_is_exact(key[i])) again |= 1u << i;
                 }
-                g += __popc(above[i]);
+                g += __popc(ba);
                 e += __popc(be);
             }
             if (__any_sync(kFull, again != 0)) {
@@ -364,10 +367,10 @@ evict_select_kernel(const EvictParams p) {
 #pragma unroll
                 for (int i = 0; i < kKeys; ++i) {
                     if (i >= per) break;
-                    const unsigned be = equal(i);
-                    const int j = g2 + __popc(above[i] & below) + min(e2 + __popc(be & below), left);
+                    const unsigned ba = above(i), be = equal(i);
+                    const int j = g2 + __popc(ba & below) + min(e2 + __popc(be & below), left);
                     if ((again >> i & 1) && j < nw_len) nw[j] = w[base + t0 + 32 * i];
-                    g2 += __popc(above[i]);
+                    g2 += __popc(ba);
                     e2 += __popc(be);
                 }
             }
