@@ -183,7 +183,7 @@ evict_select_kernel(const EvictParams p) {
     if (one) load(0, keep_recent);
     else keep_recent();
 
-    // ---- the c-th largest key.  A row in registers: bit by bit from the highest bit in
+    // ---- the c-th largest key.  A row in registers: by two bits from the highest bit in
     // which its keys differ, by counting the keys not below a candidate, until exactly c
     // are; once kList keys or fewer share the prefix those go on alone, in one
     // warp.  A longer row: three digits by histograms, one reading of the row each.
