@@ -28,7 +28,8 @@
 // up to the prefix's last, kt + gap after it) are left out.  A block of a walked tile
 // that none of the pair's rows attends is copied from past the pool's end, which TMA
 // fills with zeros: its table entry is not looked at.
-// A unit without a partner splits its tiles instead: group 0 takes the even tiles,
+// A unit without a partner (the odd one of a sequence; every unit where there are SMs for
+// all) splits its tiles instead: group 0 takes the even tiles,
 // group 1 the odd ones, and group 0 merges the two partial results at the end.
 // Every hand-off is an mbarrier or a counter and every wait is bounded, as in prefill.cu.
 //
@@ -826,7 +827,9 @@ extern "C" pkv_status pkv_paged_prefill_scoremod(
     // Where every unit can have an SM of its own (sum_s ceil(C_s g / 128) <= T g / 128 + S),
     // units stand alone and split their tiles: half the tiles one after the other.
     // Chunks of 273, 542, 14 and 606 tokens of 8 / 4 heads of 64: 13.6 us, in pairs 19.6;
-    // past one unit per SM the pairs, which read a K/V tile once for both, are as fast.
+    // 900 tokens at 3000: 48.0, in pairs 85.7.  With more units than SMs the pairs, which
+    // read a K/V tile once for both, mostly win (200 units of 8 / 4 heads of 128 at 6000:
+    // 199 us against 244).
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
