@@ -220,3 +220,38 @@ def test_units_of_many_sequences(S):
     d = setup(ctx, chunks, 4, 2, 64, 16, F16, 53)
     out = run(d, 0.125, softcap=10.0)
     check(d, out, 0.125, 10.0)
+
+
+@pytest.mark.parametrize("mods", MODS, ids=lambda m: "_".join(f"{k}{v}" for k, v in m.items()) or "plain")
+@pytest.mark.parametrize("types", [(32, 8, 128, 16, BF16), (16, 16, 64, 32, F16), (16, 16, 128, 16, BF16)],
+                         ids=lambda t: "%dx%d_D%d_b%d_%s" % (*t[:4], str(t[4])[6:]))
+def test_more_units_than_sms(types, mods):
+    """Units in pairs: each kv head's rows alone would not fit one unit per SM (148)."""
+    Hq, Hkv, D, bs, dtype = types
+    ctx, chunks = [0, 300, 37, 0, 700, 64, 0], [200, 129, 1, 0, 106, 64, 300 if Hq > Hkv else 600]
+    assert (sum(chunks) * (Hq // Hkv) // 128 + len(ctx)) * Hkv > 160
+    mods = dict(mods)
+    prefix = mods.pop("prefix", 0)
+    prefixes = [prefix] * len(ctx) if prefix else None
+    if prefix == 140:
+        prefixes = [140, 17, -3, 5, 64, 0, 300]
+    slopes = torch.linspace(0.02, 0.7, Hq).cuda() if mods.pop("alibi", False) else None
+    d = setup(ctx, chunks, Hq, Hkv, D, bs, dtype, 61, mods.get("window", 0), prefixes, qscale=2.0)
+    pre = None if prefixes is None else torch.tensor(prefixes, dtype=torch.int32).cuda()
+    scale = 1 / D ** 0.5
+    out = run(d, scale, alibi_slopes=slopes, prefix_lens=pre, **mods)
+    check(d, out, scale, slopes=slopes, prefixes=prefixes, **mods)
+
+
+def test_pairs_with_the_reference_moving_on_every_tile():
+    for grow in (True, False):  # keys that grow along the sequence, and keys that shrink (with a bias)
+        d = setup([0, 100, 0], [250, 140, 300], 32, 8, 128, 16, BF16, 62)
+        for s, L in enumerate(d["lens"].tolist()):
+            t = torch.arange(L, device="cuda")
+            f = (1 + (t if grow else L - t) / 8)[:, None, None]
+            rows = (d["kc"][d["tables"][s, t // 16].long(), t % 16].float() * f).to(BF16)
+            d["kc"][d["tables"][s, t // 16].long(), t % 16] = rows
+            d["K"][s] = rows.double().cpu().numpy()
+        slopes = None if grow else torch.linspace(0.01, 0.1, 32).cuda()
+        out = run(d, 0.2, alibi_slopes=slopes, softcap=30.0 if grow else 0.0)
+        check(d, out, 0.2, 30.0 if grow else 0.0, 0, slopes)
