@@ -255,3 +255,17 @@ def test_pairs_with_the_reference_moving_on_every_tile():
         slopes = None if grow else torch.linspace(0.01, 0.1, 32).cuda()
         out = run(d, 0.2, alibi_slopes=slopes, softcap=30.0 if grow else 0.0)
         check(d, out, 0.2, 30.0 if grow else 0.0, 0, slopes)
+
+
+@pytest.mark.parametrize("stop_tile", [0, 1, 3])
+@pytest.mark.parametrize("bias", [False, True])
+def test_bounded_waits_of_pairs_run_out(stop_tile, bias):
+    d = setup([0, 300, 1000], [300, 200, 106], 32, 8, 128, 16, BF16, 63, 300)
+    slopes = torch.linspace(0.02, 0.7, 32).cuda() if bias else None
+    out = torch.full_like(d["q"], 55.0)
+    assert pkv.lib().pkv_testing_prefill_timeout(stop_tile, 1_000_000) == pkv.PKV_OK
+    pkv.paged_prefill_scoremod(out, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], d["qs"], 0.09, window=300,
+                               alibi_slopes=slopes)
+    assert pkv.get_device_error() == pkv.DEVERR_TIMEOUT
+    out = run(d, 0.09, window=300, alibi_slopes=slopes)
+    check(d, out, 0.09, 0.0, 300, slopes)
