@@ -456,6 +456,7 @@ __device__ inline int64_t group_tile_base(const Lens<false>& ln, int g, int tt) 
 template <typename QT, int D, int NT>
 __global__ void __launch_bounds__(256)
 pkv_cascade_combine_kernel(const DecodeParams p, const CascadeParams c) {
+    const WaitPrimaryAtExit<true> wait_at_exit;  // out also holds what the passes before wrote
     // a programmatic dependent of the suffix pass's merge: every partial (the
     // prefix pass's included, which the suffix pass waited for) is complete
     // and visible after the wait; before it, only what the setup pass wrote
@@ -560,6 +561,7 @@ pkv_cascade_combine_kernel(const DecodeParams p, const CascadeParams c) {
 template <typename QT, int D, int NT>
 __global__ void __launch_bounds__(256)
 pkv_cascade_finish_kernel(const DecodeParams p, const CascadeParams c) {
+    const WaitPrimaryAtExit<true> wait_at_exit;  // out also holds what the suffix pass wrote
     constexpr int R = 8 * NT;
     constexpr int PER = D / 32;
     const int s = blockIdx.x;

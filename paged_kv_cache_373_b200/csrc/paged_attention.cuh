@@ -1438,10 +1438,12 @@ __device__ __forceinline__ void issue_tile(const DecodeParams& p, const Walk<C::
 // ----------------------------------------------------------------------------
 // kSuffix: the cascade suffix pass (per-sequence start tokens, partial
 // output); false compiles the plain decode path without either.
-// The cascade suffix pass is a programmatic dependent of the prefix pass,
-// whose results it does not read: it may run beside the prefix pass's last
-// CTAs, but it completes only after that grid, so that the passes after it
-// see every prefix partial.  Every exit of a suffix CTA waits.
+// A programmatic dependent may end before the grid it depends on unless it waits
+// for it, and what is launched next waits for the dependent alone.  So every exit
+// of such a grid's threads waits, also of those that read nothing of that grid:
+// the merge passes, and the cascade's suffix pass, which may run beside the prefix
+// pass's last CTAs but completes only after that grid, so that the passes after
+// it see every prefix partial.
 template <bool kWait>
 struct WaitPrimaryAtExit {
     __device__ ~WaitPrimaryAtExit() {
@@ -1605,8 +1607,9 @@ template <typename QT, int D, int TT, class Arg>
 __global__ void __launch_bounds__(256)
 pkv_merge_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
     constexpr bool kSuffix = Arg::kSuffix;
-    // what follows may read what the decode grid wrote: this grid may not end before it
-    const WaitPrimaryAtExit<Arg::kWeights || Arg::kMod> wait_at_exit;
+    // what follows may read what the decode grid wrote: this grid may not end before it,
+    // whether or not a unit was cut
+    const WaitPrimaryAtExit<true> wait_at_exit;
     // a following programmatic dependent (the cascade's combine pass) may be
     // scheduled now; it waits for this grid before reading
     if constexpr (kSuffix || Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1734,7 +1737,7 @@ template <typename QT, int D, int TT, class Arg>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
     constexpr bool kSuffix = Arg::kSuffix;
-    const WaitPrimaryAtExit<Arg::kWeights || Arg::kMod> wait_at_exit;
+    const WaitPrimaryAtExit<true> wait_at_exit;  // (as pkv_merge_kernel)
     // a following programmatic dependent (the cascade's combine pass) may be
     // scheduled now; it waits for this grid before reading
     if constexpr (kSuffix || Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
