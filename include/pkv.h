@@ -311,10 +311,13 @@ pkv_status pkv_paged_attention_decode_scoremod(
  * weights_out itself, else they must not overlap.  A sequence longer than
  * weight_len sets PKV_DEVERR_SEQ_LEN (its first weight_len entries are written).
  * The weights are fp32 sums of fp32 probabilities in a fixed order (no atomics);
- * out is as pkv_paged_attention_decode gives it.
+ * out is as pkv_paged_attention_decode gives it, from the same sums and roundings (its
+ * parts may be added in another order, so a last bit may differ).
  * workspace: >= pkv_paged_attention_weights_workspace_bytes(..., max_tokens =
- * max_blocks_per_seq * block_size, num_ctas) bytes (the split scratch plus one
- * fp32 score per q head and table slot), 16-byte aligned, no initialisation.
+ * max_blocks_per_seq * block_size, num_ctas) bytes (the split scratch and its sums,
+ * plus one fp32 score per q head and table slot, whatever the lengths: 1 GB for
+ * 256 sequences of 32 heads with tables of 32768 tokens), 16-byte aligned, no
+ * initialisation.
  * The size function returns 0 for invalid shapes.
  */
 size_t pkv_paged_attention_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,

@@ -102,7 +102,7 @@ pkv_status launch_decode_k(const DecodeLaunchArgs& a, const Arg& sx, cudaStream_
                 with_weights = ctas <= 2 * (int64_t)a.grid && p.g <= kWeightGroup;
                 if (with_weights) {
                     cfg.gridDim = dim3((unsigned)(units + ctas));
-                    e = cudaLaunchKernelEx(&cfg, pkv_merge_weights_kernel<typename C::q_t, C::D, C::kTT>, p, workers, sx);
+                    e = cudaLaunchKernelEx(&cfg, pkv_merge_weights_kernel<typename C::q_t, C::D, C::kTT, Arg>, p, workers, sx);
                 }
             }
             if (!with_weights)

@@ -65,14 +65,16 @@ pkv_weights_kernel(const DecodeParams p, const WeightsArg a) {
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct WeightsLayout {
-    size_t lse, scores, total;
+    size_t seg_mu, lse, scores, total;
 };
 bool weights_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int64_t max_tokens, int num_ctas,
                     WeightsLayout* l) {
     const size_t dec = decode_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, num_ctas);
     if (dec == 0 || max_tokens <= 0 || max_tokens > 0x7fffffffLL) return false;
     const size_t rows = (size_t)num_seqs * num_heads;
-    l->lse = align256(dec);
+    l->seg_mu = align256(dec);
+    l->lse = l->seg_mu + align256(decode_segment_rows(num_seqs, num_heads, num_kv_heads, head_dim, num_ctas) *
+                                  sizeof(float2));
     l->scores = l->lse + align256(rows * sizeof(float));
     l->total = l->scores + rows * (size_t)max_tokens * sizeof(float);
     return true;
@@ -156,8 +158,8 @@ extern "C" pkv_status pkv_paged_attention_decode_weights(
     if (workspace_bytes < l.total)
         return fail(PKV_EINVAL, "workspace too small: %zu < %zu bytes", workspace_bytes, l.total);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const WeightsArg w{reinterpret_cast<float*>(ws + l.scores), reinterpret_cast<float*>(ws + l.lse), max_tokens,
-                       weights_in, weights_out, weight_len,
+    const WeightsArg w{reinterpret_cast<float*>(ws + l.scores), reinterpret_cast<float*>(ws + l.lse),
+                       reinterpret_cast<float2*>(ws + l.seg_mu), max_tokens, weights_in, weights_out, weight_len,
                        weight_len % 4 == 0 && aligned16(weights_in) && aligned16(weights_out)};
     DecodeLaunchArgs a{&p, grid};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -15,6 +15,6 @@ pkv_status launch_mod_f16(const DecodeLaunchArgs& a, const ModArg& m, int head_d
     return dispatch(a, m, head_dim, s);
 }
 pkv_status launch_scores_f16(const DecodeLaunchArgs& a, const WeightsArg& w, int head_dim, cudaStream_t s) {
-    return dispatch(a, w, head_dim, s);
+    return dispatch(a, WeightsArg2{w}, head_dim, s);
 }
 }  // namespace pkv

@@ -19,6 +19,6 @@ pkv_status launch_mod_fp8(const DecodeLaunchArgs& a, const ModArg& m, bool q_bf1
     return dispatch(a, m, q_bf16, s);
 }
 pkv_status launch_scores_fp8(const DecodeLaunchArgs& a, const WeightsArg& w, bool q_bf16, cudaStream_t s) {
-    return dispatch(a, w, q_bf16, s);
+    return dispatch(a, WeightsArg2{w}, q_bf16, s);
 }
 }  // namespace pkv

@@ -71,11 +71,11 @@ struct DecodeParams {
 // first token attended per sequence, and for sequences with a non-zero start
 // the unnormalised o and (m, l) partials that replace out.
 template <bool kSuffix_> struct SuffixArg {
-    static constexpr bool kSuffix = false, kMod = false, kWeights = false;
+    static constexpr bool kSuffix = false, kMod = false, kWeights = false, kTwoSums = false;
     static constexpr const int32_t* seq_start = nullptr;
 };
 template <> struct SuffixArg<true> {
-    static constexpr bool kSuffix = true, kMod = false, kWeights = false;
+    static constexpr bool kSuffix = true, kMod = false, kWeights = false, kTwoSums = false;
     const int32_t* seq_start;  // [num_seqs]
     float* part_o;             // [num_seqs * num_heads * D]
     float2* part_ml;           // [num_seqs * num_heads]
@@ -95,7 +95,7 @@ template <> struct SuffixArg<true> {
 // kernel works in the log2 domain: x log2(e) = cap2 tanh(x log2(e) / cap2)
 // with cap2 = cap log2(e), and the slopes are scaled as they are loaded.
 struct ModArg {
-    static constexpr bool kSuffix = false, kMod = true, kWeights = false;
+    static constexpr bool kSuffix = false, kMod = true, kWeights = false, kTwoSums = false;
     const float* slopes;         // [num_heads] or null
     const int32_t* prefix_lens;  // [num_seqs] or null
     float cap2, inv_cap2;        // 0: no cap
@@ -108,14 +108,22 @@ struct ModArg {
 // pkv_weights_kernel makes the probabilities.  Storing the scores (4 bytes a
 // head and token, written and read once) costs less than reading K again.
 struct WeightsArg {
-    static constexpr bool kSuffix = false, kMod = false, kWeights = true;
+    static constexpr bool kSuffix = false, kMod = false, kWeights = true, kTwoSums = false;
     float* scores;
     float* lse;
+    float2* seg_mu;    // [segments * hpu] (kTwoSums): (m, u) of split units
     int64_t stride;    // max_blocks_per_seq * block_size
     const float* in;   // [num_seqs, num_kv_heads, len]: the weights so far, or null (zeros)
     float* out;        // and with this step's added
     int64_t len;
     bool vec;          // in and out rows are 16-byte aligned
+};
+// Where P goes to the tensor core in one 16-bit part (f16 and FP8 caches), a row has two
+// sums: l of the rounded P, which the output is divided by (what the roundings have in
+// common with its numerator's cancels), and u of P before its rounding, which the fp32
+// weights are divided by.  Kept apart, so that each pass reads one pair as before.
+struct WeightsArg2 : WeightsArg {
+    static constexpr bool kTwoSums = true;
 };
 
 // The cascade's prefix and suffix passes side by side on disjoint SMs: of a
@@ -752,6 +760,7 @@ template <> struct TileInfo<WeightsArg> {
     int64_t stride;  // floats between heads
     int nh;
 };
+template <> struct TileInfo<WeightsArg2> : TileInfo<WeightsArg> {};
 
 // ---- 16-bit caches (f16 / bf16) and FP8 caches: tensor-core tile math --------
 template <class C>
@@ -765,6 +774,7 @@ struct MmaConsumer {
     uint32_t qf[KS][2];  // B fragments of q^T (heads = gid)
     float acc[MT][4];    // O^T fragments
     float m0, m1, l0, l1;
+    float u0, u1;        // kTwoSums: the sums of P before its rounding
     float sl0, sl1;      // per-head score multipliers (log2 domain)
     // This lane's swizzled byte offsets inside a tile, fixed for the kernel:
     // 16-bit path: ldmatrix row addresses of k-step / head_dim tile k4 (mod 4)
@@ -796,7 +806,7 @@ struct MmaConsumer {
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
+        l0 = l1 = u0 = u1 = 0.f;
     }
 
     // q rows of the unit from shared memory; heads >= nh are zero.
@@ -956,6 +966,10 @@ struct MmaConsumer {
             m1 = mn1;
             l0 *= al0;
             l1 *= al1;
+            if constexpr (Arg::kTwoSums) {
+                u0 *= al0;
+                u1 *= al1;
+            }
 #pragma unroll
             for (int mi = 0; mi < MT; ++mi) {
                 acc[mi][0] *= al0; acc[mi][1] *= al1; acc[mi][2] *= al0; acc[mi][3] *= al1;
@@ -981,14 +995,12 @@ struct MmaConsumer {
                 ls0 += e0 + e2;
                 ls1 += e1 + e3;
             } else {
-                if constexpr (Arg::kWeights) {  // the weights' normaliser: P before its rounding
-                    ls0 += e0 + e2;
-                    ls1 += e1 + e3;
-                }
                 const float2 p0 = unpack2<false>(X0), p1 = unpack2<false>(X1);
-                if constexpr (!Arg::kWeights) {
-                    ls0 += p0.x + p1.x;  // normaliser from the rounded P actually used
-                    ls1 += p0.y + p1.y;
+                ls0 += p0.x + p1.x;  // normaliser from the rounded P actually used
+                ls1 += p0.y + p1.y;
+                if constexpr (Arg::kTwoSums) {
+                    u0 += e0 + e2;
+                    u1 += e1 + e3;
                 }
                 c0[m] = c1[m] = 0u;
             }
@@ -1051,9 +1063,24 @@ struct MmaConsumer {
         }
         const int h0 = 2 * tig, h1 = 2 * tig + 1;
         if constexpr (Arg::kWeights) {
-            if (!k.split && gid == 0) {
-                if (h0 < k.nh) sx.lse[k.row0 + h0] = m0 + log2f(a0);
-                if (h1 < k.nh) sx.lse[k.row0 + h1] = m1 + log2f(a1);
+            float w0 = a0, w1 = a1;
+            if constexpr (Arg::kTwoSums) {
+                w0 = u0;
+                w1 = u1;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    w0 += __shfl_xor_sync(kFull, w0, o);
+                    w1 += __shfl_xor_sync(kFull, w1, o);
+                }
+            }
+            if (gid == 0) {
+                if (!k.split) {
+                    if (h0 < k.nh) sx.lse[k.row0 + h0] = m0 + log2f(w0);
+                    if (h1 < k.nh) sx.lse[k.row0 + h1] = m1 + log2f(w1);
+                } else if constexpr (Arg::kTwoSums) {
+                    if (h0 < k.nh) sx.seg_mu[k.seg * p.hpu + h0] = make_float2(m0, w0);
+                    if (h1 < k.nh) sx.seg_mu[k.seg * p.hpu + h1] = make_float2(m1, w1);
+                }
             }
         }
         bool to_out = !k.split;
@@ -1664,20 +1691,22 @@ pkv_merge_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
     const int64_t row0 = (int64_t)hit.s * p.num_heads + (int64_t)kh * p.g + kHeadsPerUnit * c;
     constexpr int PER = D / 32;
     constexpr int kBatch = 4;
-    float M = -INFINITY, ls = 0.f, o[PER];
+    float M = -INFINITY, ls = 0.f, lw = 0.f, o[PER];  // lw: the weights' normaliser (kTwoSums)
 #pragma unroll
     for (int e = 0; e < PER; ++e) o[e] = 0.f;
     for (int64_t w0 = bf; w0 <= bl; w0 += kBatch) {
         float2 ml[kBatch];
-        float v[kBatch][PER];
+        float v[kBatch][PER], wl[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int64_t w = w0 + k;
             ml[k] = make_float2(-INFINITY, 0.f);
+            wl[k] = 0.f;
 #pragma unroll
             for (int e = 0; e < PER; ++e) v[k][e] = 0.f;
             if (w <= bl) {
                 ml[k] = p.ws_ml[(w + u) * p.hpu + h];
+                if constexpr (Arg::kTwoSums) wl[k] = sx.seg_mu[(w + u) * p.hpu + h].y;
                 const float* src = p.ws_o + ((w + u) * p.hpu + h) * D;
 #pragma unroll
                 for (int e = 0; e < PER; ++e) v[k][e] = src[lane + 32 * e];
@@ -1689,12 +1718,14 @@ pkv_merge_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
         if (Mb == -INFINITY) continue;  // nothing attended yet
         const float fo = M == -INFINITY ? 0.f : ex2(M - Mb);
         ls *= fo;
+        if constexpr (Arg::kTwoSums) lw *= fo;
 #pragma unroll
         for (int e = 0; e < PER; ++e) o[e] *= fo;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - Mb);
             ls += ml[k].y * f;
+            if constexpr (Arg::kTwoSums) lw += wl[k] * f;
 #pragma unroll
             for (int e = 0; e < PER; ++e) o[e] += v[k][e] * f;
         }
@@ -1709,7 +1740,7 @@ pkv_merge_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
         }
     }
     if constexpr (Arg::kWeights)
-        if (lane == 0) sx.lse[row0 + h] = M + log2f(ls);
+        if (lane == 0) sx.lse[row0 + h] = M + log2f(Arg::kTwoSums ? lw : ls);
     QT* out = reinterpret_cast<QT*>(p.out) + (row0 + h) * D;
 #pragma unroll
     for (int e = 0; e < PER; ++e) out[lane + 32 * e] = from_f32<QT>(ls > 0.f ? o[e] / ls : 0.f);
@@ -1806,20 +1837,22 @@ pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
         int tw = 0, h = q;
         while (h >= task_nh[tw]) h -= task_nh[tw++];
         const MergeTask t = tasks[tw];
-        float M = -INFINITY, ls = 0.f, o[PER];
+        float M = -INFINITY, ls = 0.f, lw = 0.f, o[PER];  // lw: the weights' normaliser (kTwoSums)
 #pragma unroll
         for (int e = 0; e < PER; ++e) o[e] = 0.f;
         for (int64_t w0 = t.bf; w0 <= t.bl; w0 += kBatch) {
             float2 ml[kBatch];
-            float v[kBatch][PER];
+            float v[kBatch][PER], wl[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int64_t w = w0 + k;
                 ml[k] = make_float2(-INFINITY, 0.f);
+                wl[k] = 0.f;
 #pragma unroll
                 for (int e = 0; e < PER; ++e) v[k][e] = 0.f;
                 if (w <= t.bl) {
                     ml[k] = p.ws_ml[(w + t.u) * p.hpu + h];
+                    if constexpr (Arg::kTwoSums) wl[k] = sx.seg_mu[(w + t.u) * p.hpu + h].y;
                     const float* src = p.ws_o + ((w + t.u) * p.hpu + h) * D;
 #pragma unroll
                     for (int e = 0; e < PER; ++e) v[k][e] = src[lane + 32 * e];
@@ -1831,12 +1864,14 @@ pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
             if (Mb == -INFINITY) continue;  // nothing attended yet
             const float fo = M == -INFINITY ? 0.f : ex2(M - Mb);
             ls *= fo;
+            if constexpr (Arg::kTwoSums) lw *= fo;
 #pragma unroll
             for (int e = 0; e < PER; ++e) o[e] *= fo;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - Mb);
                 ls += ml[k].y * f;
+                if constexpr (Arg::kTwoSums) lw += wl[k] * f;
 #pragma unroll
                 for (int e = 0; e < PER; ++e) o[e] += v[k][e] * f;
             }
@@ -1851,7 +1886,7 @@ pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
             }
         }
         if constexpr (Arg::kWeights)
-            if (lane == 0) sx.lse[t.row0 + h] = M + log2f(ls);
+            if (lane == 0) sx.lse[t.row0 + h] = M + log2f(Arg::kTwoSums ? lw : ls);
         QT* out = reinterpret_cast<QT*>(p.out) + (t.row0 + h) * D;
 #pragma unroll
         for (int e = 0; e < PER; ++e) out[lane + 32 * e] = from_f32<QT>(ls > 0.f ? o[e] / ls : 0.f);
@@ -1868,11 +1903,14 @@ pkv_merge_wide_kernel(const DecodeParams p, int64_t workers, const Arg sx) {
 // combined through shared memory.  The order is fixed by the split alone.
 // ----------------------------------------------------------------------------
 constexpr int kUnitWarps = 8, kFold = 8;
-template <typename QT, int D, int TT, class Arg>
+// kLse: also the row's log sum, for a weights pass that follows.
+template <typename QT, int D, int TT, bool kLse, class Arg>
 __device__ __forceinline__ void merge_unit(const DecodeParams& p, int64_t workers, const Arg& ax, int64_t unit) {
     constexpr int PER = D / 32;
+    constexpr bool kTwo = kLse && Arg::kTwoSums;
     __shared__ float part_o[kUnitWarps][D];
     __shared__ float2 part_ml[kUnitWarps];
+    __shared__ float part_w[kUnitWarps];
     __shared__ int64_t first_last[2];  // the unit's first and last worker; none if it has no tiles
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const auto ln = make_lens<TT>(p, ax);
@@ -1904,21 +1942,23 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, int64_t worker
     const int h = warp % nh, part = warp / nh;
     const int64_t u = ((int64_t)s * p.num_kv_heads + kh) * p.nch + c;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float M = -INFINITY, ls = 0.f, o[PER];
+    float M = -INFINITY, ls = 0.f, lw = 0.f, o[PER];  // lw: the weights' normaliser (kTwo)
 #pragma unroll
     for (int e = 0; e < PER; ++e) o[e] = 0.f;
     if (part < parts) {
         for (int64_t w0 = bf + part; w0 <= bl; w0 += kFold * parts) {
             float2 ml[kFold];
-            float v[kFold][PER];
+            float v[kFold][PER], wl[kFold];
 #pragma unroll
             for (int k = 0; k < kFold; ++k) {
                 const int64_t w = w0 + k * parts;
                 ml[k] = make_float2(-INFINITY, 0.f);
+                wl[k] = 0.f;
 #pragma unroll
                 for (int e = 0; e < PER; ++e) v[k][e] = 0.f;
                 if (w <= bl) {
                     ml[k] = p.ws_ml[(w + u) * p.hpu + h];
+                    if constexpr (kTwo) wl[k] = ax.seg_mu[(w + u) * p.hpu + h].y;
                     const float* src = p.ws_o + ((w + u) * p.hpu + h) * D;
 #pragma unroll
                     for (int e = 0; e < PER; ++e) v[k][e] = src[lane + 32 * e];
@@ -1930,12 +1970,14 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, int64_t worker
             if (Mb == -INFINITY) continue;  // nothing attended yet
             const float fo = ex2(M - Mb);
             ls *= fo;
+            if constexpr (kTwo) lw *= fo;
 #pragma unroll
             for (int e = 0; e < PER; ++e) o[e] *= fo;
 #pragma unroll
             for (int k = 0; k < kFold; ++k) {
                 const float f = ex2(ml[k].x - Mb);
                 ls += ml[k].y * f;
+                if constexpr (kTwo) lw += wl[k] * f;
 #pragma unroll
                 for (int e = 0; e < PER; ++e) o[e] += v[k][e] * f;
             }
@@ -1943,7 +1985,10 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, int64_t worker
         }
     }
     if (parts > 1) {
-        if (lane == 0) part_ml[warp] = make_float2(M, ls);
+        if (lane == 0) {
+            part_ml[warp] = make_float2(M, ls);
+            if constexpr (kTwo) part_w[warp] = lw;
+        }
 #pragma unroll
         for (int e = 0; e < PER; ++e) part_o[warp][lane + 32 * e] = o[e];
         __syncthreads();
@@ -1952,20 +1997,22 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, int64_t worker
         for (int k = 1; k < parts; ++k) Mb = fmaxf(Mb, part_ml[h + k * nh].x);
         const float fo = M == -INFINITY ? 0.f : ex2(M - Mb);
         ls *= fo;
+        if constexpr (kTwo) lw *= fo;
 #pragma unroll
         for (int e = 0; e < PER; ++e) o[e] *= fo;
         for (int k = 1; k < parts; ++k) {
             const float2 ml = part_ml[h + k * nh];
             const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mb);
             ls += ml.y * f;
+            if constexpr (kTwo) lw += part_w[h + k * nh] * f;
 #pragma unroll
             for (int e = 0; e < PER; ++e) o[e] += part_o[h + k * nh][lane + 32 * e] * f;
         }
         M = Mb;
     }
     if (part > 0) return;
-    if constexpr (Arg::kWeights)
-        if (lane == 0) ax.lse[row0 + h] = M + log2f(ls);
+    if constexpr (kLse)
+        if (lane == 0) ax.lse[row0 + h] = M + log2f(kTwo ? lw : ls);
 #pragma unroll
     for (int e = 0; e < PER; ++e) out[h * D + lane + 32 * e] = from_f32<QT>(ls > 0.f ? o[e] / ls : 0.f);
 }
@@ -1975,7 +2022,7 @@ __global__ void __launch_bounds__(kUnitWarps * 32)
 pkv_merge_units_kernel(const DecodeParams p, int64_t workers, const Arg ax) {
     if constexpr (Arg::kWeights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const WaitPrimaryAtExit<true> wait_at_exit;  // this grid may not end before the decode grid
-    merge_unit<QT, D, TT>(p, workers, ax, blockIdx.x);
+    merge_unit<QT, D, TT, Arg::kWeights>(p, workers, ax, blockIdx.x);
 }
 
 // ----------------------------------------------------------------------------
@@ -2049,18 +2096,20 @@ __device__ __forceinline__ void weights_item(const DecodeParams& p, const Weight
 // (m, l) themselves, so neither waits for the other (one launch and one grid's
 // latency less).
 constexpr int kWeightGroup = 256;  // q heads per kv head that it can hold
-template <typename QT, int D, int TT>
+template <typename QT, int D, int TT, class Arg>
 __global__ void __launch_bounds__(kUnitWarps * 32)
-pkv_merge_weights_kernel(const DecodeParams p, int64_t workers, const WeightsArg a) {
+pkv_merge_weights_kernel(const DecodeParams p, int64_t workers, const Arg a) {
     const WaitPrimaryAtExit<true> wait_at_exit;
     const auto ln = make_lens<TT>(p, a);
     const int64_t units = (int64_t)p.num_seqs * ln.units;
     if (blockIdx.x < units) {
-        merge_unit<QT, D, TT>(p, workers, a, blockIdx.x);
+        merge_unit<QT, D, TT, false>(p, workers, a, blockIdx.x);
         return;
     }
     constexpr int kTokens = kUnitWarps * 32 * 4;
     __shared__ float lse[kWeightGroup];
+    const float2* seg = p.ws_ml;  // the split units' (m, l), or (m, u)
+    if constexpr (Arg::kTwoSums) seg = a.seg_mu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Lens<false> items{p.seq_lens, nullptr, p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq * p.block_size};
     const int64_t ctas = gridDim.x - units, WI = total_tiles<kTokens>(items);
@@ -2090,7 +2139,7 @@ pkv_merge_weights_kernel(const DecodeParams p, int64_t workers, const WeightsArg
                 const int64_t u = ((int64_t)w.s * p.num_kv_heads + w.j) * p.nch + c;
                 float M = -INFINITY, l = 0.f;
                 for (int64_t k = bf + lane; k <= bl; k += 32) {
-                    const float2 ml = p.ws_ml[(k + u) * p.hpu + h];
+                    const float2 ml = seg[(k + u) * p.hpu + h];
                     const float m = fmaxf(M, ml.x);
                     l = l * ex2(M - m) + ml.y * ex2(ml.x - m);
                     M = m;

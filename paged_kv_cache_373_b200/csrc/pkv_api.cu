@@ -99,7 +99,7 @@ static int default_ctas() {
 }
 
 struct WsLayout {
-    size_t o_bytes, ml_off, total;
+    size_t o_bytes, ml_off, total, rows;  // rows: segments * hpu
     int hpu, nch, grid;
 };
 
@@ -114,9 +114,10 @@ static bool ws_layout(int num_seqs, int num_heads, int num_kv_heads, int head_di
     w->hpu = g < kHeadsPerUnit ? g : kHeadsPerUnit;
     // one segment per worker (up to kMaxWarpsPerCta warps per CTA) plus one per unit
     const size_t segs = (size_t)w->grid * kMaxWarpsPerCta + (size_t)num_seqs * num_kv_heads * w->nch;
-    w->o_bytes = segs * w->hpu * head_dim * sizeof(float);
+    w->rows = segs * w->hpu;
+    w->o_bytes = w->rows * head_dim * sizeof(float);
     w->ml_off = (w->o_bytes + 255) & ~(size_t)255;
-    w->total = w->ml_off + segs * w->hpu * sizeof(float2);
+    w->total = w->ml_off + w->rows * sizeof(float2);
     return true;
 }
 
@@ -213,6 +214,12 @@ size_t decode_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int
     WsLayout w;
     if (!ws_layout(num_seqs, num_heads, num_kv_heads, head_dim, num_ctas, &w)) return 0;
     return w.total;
+}
+
+size_t decode_segment_rows(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_ctas) {
+    WsLayout w;
+    if (!ws_layout(num_seqs, num_heads, num_kv_heads, head_dim, num_ctas, &w)) return 0;
+    return w.rows;
 }
 
 }  // namespace pkv

@@ -60,6 +60,8 @@ pkv_status decode_prepare(DecodeParams* p, DecodeLauncher* launch, int* grid, vo
                           const float* k_scale, const float* v_scale, void* workspace,
                           size_t workspace_bytes, int num_ctas);
 size_t decode_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_ctas);
+// (m, l) entries in it: one per segment and q head of a unit.
+size_t decode_segment_rows(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_ctas);
 
 // One launcher per kernel variant (attn_*.cu).
 pkv_status launch_decode_f32_d64(const DecodeLaunchArgs&, cudaStream_t);
