@@ -351,9 +351,11 @@ pkv_status pkv_paged_attention_decode_weights(
  * old blocks, which may be shared with other sequences, are left as they are and can
  * be released once the stream has passed the call).
  * weights: DEVICE fp32 [num_seqs, num_kv_heads, weight_len]; new_weights: DEVICE fp32
- * [num_seqs, num_kv_heads, new_weight_len], not overlapping weights; kept: DEVICE int32
+ * [num_seqs, num_kv_heads, new_weight_len]; kept: DEVICE int32
  * [num_seqs, num_kv_heads, budget]; new_block_tables: DEVICE int32 [num_seqs,
- * new_max_blocks_per_seq]; new_seq_lens: DEVICE int32 [num_seqs], not seq_lens.
+ * new_max_blocks_per_seq]; new_seq_lens: DEVICE int32 [num_seqs].  new_seq_lens,
+ * new_weights and kept must not overlap seq_lens, weights, the tables or one another
+ * (PKV_EINVAL).
  * A seq_len below 0, longer than its table row or than weight_len (it is clamped), a
  * new table shorter than the budget or new_weight_len below n (what does not fit is not
  * written) sets PKV_DEVERR_SEQ_LEN; a block id out of range (those rows are skipped)

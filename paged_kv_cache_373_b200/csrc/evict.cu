@@ -443,6 +443,17 @@ evict_gather_kernel(const EvictParams p, int nblk, int parts, int lg_bs) {
     }
 }
 
+// A buffer of the call; bytes as a double, which no product of its sizes overflows.
+struct Span {
+    const char* name;
+    const void* at;
+    double bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x <= y ? (double)(y - x) < a.bytes : (double)(x - y) < b.bytes;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -475,6 +486,21 @@ extern "C" pkv_status pkv_evict_tokens(void* key_cache, void* value_cache, pkv_d
     if (!aligned16(key_cache) || !aligned16(value_cache)) return fail(PKV_EINVAL, "caches must be 16-byte aligned");
     if (new_weights == weights) return fail(PKV_EINVAL, "new_weights must not be weights");
     const int64_t rows = (int64_t)num_seqs * num_kv_heads;
+    // What the call writes lies apart from all that it reads and from what else it writes: other
+    // CTAs of a sequence still read its length, table and weights when its first results are stored.
+    const Span reads[] = {{"seq_lens", seq_lens, 4.0 * num_seqs},
+                          {"weights", weights, 4.0 * rows * weight_len},
+                          {"block_tables", block_tables, 4.0 * num_seqs * max_blocks_per_seq},
+                          {"new_block_tables", new_block_tables, 4.0 * num_seqs * new_max_blocks_per_seq}};
+    const Span writes[] = {{"new_seq_lens", new_seq_lens, 4.0 * num_seqs},
+                           {"new_weights", new_weights, 4.0 * rows * new_weight_len},
+                           {"kept", kept, 4.0 * rows * budget}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span& r : reads)
+            if (overlap(writes[i], r)) return fail(PKV_EINVAL, "%s overlaps %s", writes[i].name, r.name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(writes[i], writes[j])) return fail(PKV_EINVAL, "%s overlaps %s", writes[i].name, writes[j].name);
+    }
     // destination blocks a sequence can have: as many as its new table and its tokens give
     const int64_t nblk = std::min<int64_t>(std::min<int64_t>(((int64_t)budget + block_size - 1) / block_size,
                                                              new_max_blocks_per_seq), max_blocks_per_seq);
