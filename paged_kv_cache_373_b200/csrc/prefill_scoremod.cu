@@ -99,7 +99,7 @@ enum : int {
 struct PfMod {
     const float* slopes;         // [num_heads] or null
     const int32_t* prefix_lens;  // [num_seqs] or null
-    float pre;                   // scale / cap (0: no cap)
+    float pre, inv_pre;          // scale / cap (0: no cap), cap / scale
     int window;                  // 0: no window
     int units;                   // per CTA: pairs (2), or every unit by itself (1)
 };
@@ -337,7 +337,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_addr + X * 128;
         const uint32_t tO = tmem + lane_addr + 256 + X * 128;
-        const CapCoef cap = cap_coef(kCap ? md.pre : 1.f);
+        const CapCoef cap = cap_coef(kCap ? md.pre : 1.f, kCap ? md.inv_pre : 1.f);
         const float sl2 = p.scale_log2;
         const float emul = kBias ? 1.f : sl2;  // without a bias the scale is applied in the exponent
         const float slope2 = kBias ? __ldg(md.slopes + (int64_t)kh * p.g + row % p.g) * 1.4426950408889634f : 0.f;
@@ -810,7 +810,7 @@ extern "C" pkv_status pkv_paged_prefill_scoremod(
                                     max_blocks_per_seq, seq_lens, query_start, num_seqs, num_query_tokens, num_heads,
                                     num_kv_heads, head_dim, block_size, num_blocks, scale);
     if (st != PKV_OK) return st;
-    PfMod md{alibi_slopes, prefix_lens, 0.f, window, 2};
+    PfMod md{alibi_slopes, prefix_lens, 0.f, 0.f, window, 2};
     float cap2 = 0.f, inv_cap2 = 0.f;
     st = score_cap(softcap, &cap2, &inv_cap2);
     if (st != PKV_OK) return st;
@@ -820,8 +820,16 @@ extern "C" pkv_status pkv_paged_prefill_scoremod(
     if (window >= max_blocks_per_seq * block_size) md.window = 0;  // hides nothing
     if (grid == 0) return PKV_OK;
     md.pre = p.scale_log2 * inv_cap2;
-    if (softcap > 0.f && !(md.pre > 0.f && 1.f / md.pre > 0.f && 1.f / md.pre < INFINITY && md.pre < INFINITY))
-        return fail(PKV_EINVAL, "scale / softcap outside fp32");
+    md.inv_pre = 1.f / md.pre;
+    if (softcap > 0.f && !(md.pre >= 0x1p-126f && md.pre <= 0x1p126f)) {
+        // scale / cap next to or past the ends of fp32.  Below 2^-126 the cap changes no
+        // product q.k under 2^114 in its 24 bits, and 2^-126 gives the same; above 2^126
+        // tanh is 1 for every product but 0, whichever of the two multiplies it, and
+        // what is left is the cap itself.
+        const double r = (double)scale / (double)softcap;
+        md.pre = r < 1.0 ? 0x1p-126f : 0x1p126f;
+        md.inv_pre = r < 1.0 ? 0x1p126f : (float)(1.0 / r);
+    }
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const int64_t T = num_query_tokens;
     // Where every unit can have an SM of its own (sum_s ceil(C_s g / 128) <= T g / 128 + S),

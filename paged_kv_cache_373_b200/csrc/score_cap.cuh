@@ -55,7 +55,7 @@ struct CapCoef {
     F2 c1, c2, c3;
     float pre, inv_pre, lim;  // lim: largest |x| for the polynomial (0: never)
 };
-__device__ __forceinline__ CapCoef cap_coef(float pre) {
+__device__ __forceinline__ CapCoef cap_coef(float pre, float inv_pre) {
     CapCoef k;
     const float p2 = pre * pre;
     const float a = -0.33332663774490356f * p2, b = 0.1329982578754425f * p2 * p2, c = -0.049148499965667725f * p2 * p2 * p2;
@@ -63,7 +63,7 @@ __device__ __forceinline__ CapCoef cap_coef(float pre) {
     k.c2 = f2(b, b);
     k.c3 = f2(c, c);
     k.pre = pre;
-    k.inv_pre = 1.f / pre;
+    k.inv_pre = inv_pre;
     k.lim = pre > 0x1p-14f && pre < 0x1p14f ? 0.35f / pre : 0.f;
     return k;
 }
