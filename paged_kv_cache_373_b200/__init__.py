@@ -212,6 +212,14 @@ def _scalar(t: Optional[torch.Tensor], name: str, index: int) -> Optional[int]:
     return _arg(t, name, index, torch.float32)
 
 
+def _int32(x, name: str) -> int:
+    """x as a C int (ctypes would pass on its low 32 bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} {x} does not fit 32 bits")
+    return x
+
+
 def _index(t: torch.Tensor, name: str) -> int:
     """The CUDA device of a call, from its first tensor."""
     i = t.get_device()
@@ -358,7 +366,7 @@ def paged_prefill_scoremod(out, query, key_cache, value_cache, block_tables, seq
             _arg(block_tables, "block_tables", dev, torch.int32), tshape[1],
             _arg(seq_lens, "seq_lens", dev, torch.int32, (S,)),
             _arg(query_start, "query_start", dev, torch.int32, (S + 1,)), S, T, Hq, Hkv, D, bs, NB, float(scale),
-            float(softcap), int(window), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
+            float(softcap), _int32(window, "window"), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
             _arg(prefix_lens, "prefix_lens", dev, torch.int32, (S,)))
     return out
 
@@ -454,9 +462,10 @@ def paged_attention_decode_scoremod(out, query, key_cache, value_cache, block_ta
         with torch.cuda.device(dev):
             workspace = _scratch(paged_attention_workspace_bytes(S, Hq, Hkv, D, num_ctas), dev, stream)
     _launch(lib().pkv_paged_attention_decode_scoremod, dev, stream, o, *args, float(scale), float(softcap),
-            int(window), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
+            _int32(window, "window"), _arg(alibi_slopes, "alibi_slopes", dev, torch.float32, (Hq,)),
             _arg(prefix_lens, "prefix_lens", dev, torch.int32, (S,)), _scalar(k_scale, "k_scale", dev),
-            _scalar(v_scale, "v_scale", dev), _arg(workspace, "workspace", dev), workspace.nbytes, int(num_ctas))
+            _scalar(v_scale, "v_scale", dev), _arg(workspace, "workspace", dev), workspace.nbytes,
+            _int32(num_ctas, "num_ctas"))
     return out
 
 
@@ -483,7 +492,7 @@ def paged_attention_decode_weights(out, weights_out, query, key_cache, value_cac
             workspace = _scratch(paged_attention_weights_workspace_bytes(S, Hq, Hkv, D, cap, num_ctas), dev, stream)
     _launch(lib().pkv_paged_attention_decode_weights, dev, stream, o, wo, wi, wshape[2], *args,
             float(scale), _scalar(k_scale, "k_scale", dev), _scalar(v_scale, "v_scale", dev),
-            _arg(workspace, "workspace", dev), workspace.nbytes, int(num_ctas))
+            _arg(workspace, "workspace", dev), workspace.nbytes, _int32(num_ctas, "num_ctas"))
     return out
 
 
@@ -493,7 +502,7 @@ def evict_tokens(key_cache, value_cache, block_tables, seq_lens, weights, new_bl
     kv head, moving their K/V rows to the blocks of new_block_tables (see pkv_evict_tokens).  weights
     fp32 [S, Hkv, W]; written: new_seq_lens int32 [S], new_weights fp32 [S, Hkv, W'], kept int32
     [S, Hkv, budget]."""
-    dev = _index(key_cache, "key_cache")
+    dev, budget, recent = _index(key_cache, "key_cache"), _int32(budget, "budget"), _int32(recent, "recent")
     kc, vc, cdt, (NB, bs, Hkv, D) = _caches(key_cache, value_cache, dev)
     S = seq_lens.shape[0]
     ws, nws, ts, nts = weights.shape, new_weights.shape, block_tables.shape, new_block_tables.shape
@@ -507,7 +516,7 @@ def evict_tokens(key_cache, value_cache, block_tables, seq_lens, weights, new_bl
             _arg(new_block_tables, "new_block_tables", dev, torch.int32), nts[1],
             _arg(new_seq_lens, "new_seq_lens", dev, torch.int32, (S,)),
             _arg(new_weights, "new_weights", dev, torch.float32), nws[2],
-            _arg(kept, "kept", dev, torch.int32, (S, Hkv, int(budget))), int(budget), int(recent), S, Hkv, D, bs, NB)
+            _arg(kept, "kept", dev, torch.int32, (S, Hkv, budget)), budget, recent, S, Hkv, D, bs, NB)
 
 
 STATIC_WORKSPACE_BYTES = 16 * 1024 * 1024   # PKV_STATIC_WORKSPACE_BYTES
