@@ -461,6 +461,12 @@ pkv_status pkv_paged_prefill(void* out, const void* query, pkv_dtype q_dtype, co
  *   t < min(prefix_lens[s], L), whatever p is (a prefix that sees all of itself), or
  *   t <= p with p - t < window (window = 0: every t <= p),
  * with x = scale q.K_t, capped by softcap and biased by -alibi_slopes[h] * |p - t|.
+ * So a prefix is not causal in itself: a row below it attends the prefix's later
+ * tokens, which the decode form's query, the last token, has none of.  For a causal
+ * prompt with kept first tokens a chunk with rows below the prefix lists its sequence
+ * twice (the same block_tables row twice): first those rows, with the prefix as their
+ * seq_lens and prefix_lens 0 (a window, if any, at least the prefix), then the others
+ * with the sequence's length and prefix.
  * Blocks none of whose tokens a row of the chunk attends are not read and their table
  * entries not looked at.  In the blocks that are read, tokens t < L hidden from some
  * rows must hold finite V (P = 0 is multiplied with them, as in pkv_paged_prefill);

@@ -351,7 +351,9 @@ def paged_prefill_scoremod(out, query, key_cache, value_cache, block_tables, seq
                            softcap: float = 0.0, window: int = 0, alibi_slopes=None, prefix_lens=None,
                            stream=None) -> torch.Tensor:
     """Chunked-prefill attention with modified scores (see paged_attention_decode_scoremod and
-    pkv_paged_prefill_scoremod); query/out [T, Hq, D], rows of sequence s as in paged_prefill."""
+    pkv_paged_prefill_scoremod); query/out [T, Hq, D], rows of sequence s as in paged_prefill.
+    Every row attends the whole prefix, also a row below it: a causal prompt with kept first tokens
+    lists such rows as a sequence of their own (see pkv_paged_prefill_scoremod)."""
     dev, dt, shape = _index(query, "query"), query.dtype, query.shape
     T, Hq, D = shape
     kc, vc, cdt, (NB, bs, Hkv, cd) = _caches(key_cache, value_cache, dev)
