@@ -11,7 +11,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <deque>
 #include <exception>
 #include <string>
 #include <unordered_map>
@@ -115,6 +114,28 @@ struct KeyHash {
     size_t operator()(const Key& k) const { size_t h; memcpy(&h, k.b, sizeof h); return h; }
 };
 
+// The free list: a queue with room for every block, so that releasing one never allocates.
+class FreeList {
+public:
+    void reserve(int64_t blocks) { ring_.resize(blocks); }
+    int64_t size() const { return (int64_t)size_; }
+    bool empty() const { return size_ == 0; }
+    void push_back(int32_t b) {
+        const size_t at = head_ + size_++;
+        ring_[at < ring_.size() ? at : at - ring_.size()] = b;
+    }
+    int32_t pop_front() {
+        const int32_t b = ring_[head_];
+        if (++head_ == ring_.size()) head_ = 0;
+        --size_;
+        return b;
+    }
+
+private:
+    std::vector<int32_t> ring_;
+    size_t head_ = 0, size_ = 0;
+};
+
 struct Seq {
     std::vector<int32_t> table;
     std::vector<int32_t> tokens;
@@ -132,7 +153,7 @@ struct pkv_block_manager {
     int64_t nb = 0;
     int bs = 0;
     bool cache = false;
-    std::deque<int32_t> free_list;
+    FreeList free_list;
     std::vector<int32_t> ref;
     std::vector<uint8_t> has_key;
     std::vector<Key> key_of;
@@ -160,13 +181,12 @@ struct pkv_block_manager {
         parked[b] = 0;
         --num_parked;
     }
-    int64_t available() const { return (int64_t)free_list.size() + num_parked; }
+    int64_t available() const { return free_list.size() + num_parked; }
     // caller has checked available() > 0
     int32_t take() {
         int32_t b;
         if (!free_list.empty()) {
-            b = free_list.front();
-            free_list.pop_front();
+            b = free_list.pop_front();
         } else {
             b = head;
             unpark(b);
@@ -270,6 +290,7 @@ extern "C" pkv_status pkv_bm_create(int64_t num_blocks, int block_size, const in
     bm->nb = num_blocks;
     bm->bs = block_size;
     bm->cache = prefix_cache != 0;
+    bm->free_list.reserve(num_blocks);
     bm->ref.assign(num_blocks, 0);
     bm->has_key.assign(num_blocks, 0);
     bm->key_of.resize(num_blocks);
@@ -506,7 +527,7 @@ extern "C" pkv_status pkv_bm_get_stats(const pkv_block_manager* bm, pkv_bm_stats
     pkv_bm_stats r{};
     r.num_blocks = bm->nb;
     r.block_size = bm->bs;
-    r.free_blocks = (int64_t)bm->free_list.size();
+    r.free_blocks = bm->free_list.size();
     r.parked_blocks = bm->num_parked;
     r.cached_blocks = (int64_t)bm->block_of.size();
     std::vector<int32_t> fill(bm->nb, 0);
