@@ -149,7 +149,8 @@ pkv_status pkv_reshape_and_cache(const void* key, const void* value, pkv_dtype s
  * [max_position, rotary_dim], both ignored when rotary_dim = 0 (no rotation).
  * slot_mapping entries >= 0 must be distinct.
  * dtype f32, f16 or bf16; cache_dtype the same, or FP8_E4M3 with k_scale and
- * v_scale; head_dim in {64, 128}; rotary_dim a multiple of 16 up to head_dim
+ * v_scale; head_dim in {64, 128} (the attention calls read FP8 caches with 128 only);
+ * rotary_dim a multiple of 16 up to head_dim
  * (PKV_EUNSUPPORTED otherwise).  All buffers but the scales, slots and positions
  * 16-byte aligned.
  */
@@ -346,7 +347,15 @@ pkv_status pkv_paged_attention_decode_weights(
  *   n = min(L, budget): new_seq_lens[s] = n, kept[s, h, j] = t_j for j < n and -1 for
  *     n <= j < budget, new_weights[s, h, j] = w[t_j] for j < n (the rest as it was).
  * Rows keep their rotary phase, so a rotated K needs no change; different heads of one
- * slot then hold different tokens, which attention does not mind.
+ * slot then hold different tokens, which plain attention does not mind.  But a slot's
+ * index is no longer a position: tokens appended later go to the slots from n on and
+ * keep counting their positions (for the rotary embedding) from the unshortened
+ * length, and what goes by the index -- alibi_slopes, window and prefix_lens of the
+ * scoremod calls -- counts slots, not distances, on a shortened sequence (softcap
+ * alone is not affected).  kept says which token a slot holds; no call takes it.
+ * The weights are what the caller has accumulated, from decode steps: no call adds a
+ * prompt's rows.  Right after a prompt, with weights still zero, the earliest tokens
+ * stay beside the recent ones.
  * The new blocks must be distinct and must not be blocks that the call reads (the
  * old blocks, which may be shared with other sequences, are left as they are and can
  * be released once the stream has passed the call).
@@ -360,8 +369,8 @@ pkv_status pkv_paged_attention_decode_weights(
  * new table shorter than the budget or new_weight_len below n (what does not fit is not
  * written) sets PKV_DEVERR_SEQ_LEN; a block id out of range (those rows are skipped)
  * PKV_DEVERR_BLOCK_ID.
- * cache_dtype f32, f16, bf16 or FP8_E4M3; head_dim in {64, 128}; block_size in {16, 32};
- * budget > 0; 0 <= recent <= budget.  No workspace; the result is the same bits on
+ * cache_dtype f32, f16, bf16 or FP8_E4M3; head_dim in {64, 128} (the attention calls read
+ * FP8 caches with 128 only); block_size in {16, 32}; budget > 0; 0 <= recent <= budget.  No workspace; the result is the same bits on
  * every run.
  */
 pkv_status pkv_evict_tokens(void* key_cache, void* value_cache, pkv_dtype cache_dtype,

@@ -112,7 +112,12 @@ pkv_status pkv_bm_append_batch(pkv_block_manager* bm, const int64_t* seq_ids, co
  * batch's device call reads; the old ones are released as pkv_bm_free_sequence does
  * and may be reused by work ordered after that call.  The blocks of a shortened
  * sequence no longer hold a prompt's prefix: they get no keys, also not the ones it
- * fills later.  All or nothing: PKV_ENOBLOCKS changes nothing. */
+ * fills later.  All or nothing: PKV_ENOBLOCKS changes nothing.
+ * So the batch needs room for its fresh blocks beside its old ones: ceil(budget /
+ * block_size) per shortened sequence, free or parked.  In a fuller pool go by fewer
+ * sequences at a time, the device call of one part launched before the next part's
+ * tables are taken (its old blocks are free from there on), and evict while blocks
+ * for one sequence are left. */
 pkv_status pkv_bm_evict_batch(pkv_block_manager* bm, const int64_t* seq_ids, int64_t n, int64_t budget,
                               int32_t* new_tables, int64_t new_max_blocks, int32_t* new_lens);
 

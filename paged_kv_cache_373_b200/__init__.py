@@ -502,8 +502,9 @@ def evict_tokens(key_cache, value_cache, block_tables, seq_lens, weights, new_bl
                  new_weights, kept, budget: int, recent: int, stream=None) -> None:
     """Shorten every sequence longer than `budget` to its last `recent` and its heaviest other tokens, per
     kv head, moving their K/V rows to the blocks of new_block_tables (see pkv_evict_tokens).  weights
-    fp32 [S, Hkv, W]; written: new_seq_lens int32 [S], new_weights fp32 [S, Hkv, W'], kept int32
-    [S, Hkv, budget]."""
+    fp32 [S, Hkv, W], from decode steps; written: new_seq_lens int32 [S], new_weights fp32 [S, Hkv, W'],
+    kept int32 [S, Hkv, budget], all apart from the inputs.  On a shortened sequence slots are not
+    positions: alibi_slopes, window and prefix_lens of the scoremod calls count slots there."""
     dev, budget, recent = _index(key_cache, "key_cache"), _int32(budget, "budget"), _int32(recent, "recent")
     kc, vc, cdt, (NB, bs, Hkv, D) = _caches(key_cache, value_cache, dev)
     S = seq_lens.shape[0]
@@ -702,7 +703,8 @@ class HostBlockManager:
     def evict_batch(self, sids, budget: int, new_max_blocks: int = 0):
         """Fresh blocks for every sequence longer than `budget`, which then holds `budget` tokens (for
         evict_tokens; take the old tables with batch_tables first): (new_block_tables int32
-        [n, new_max_blocks], rows of -1 for sequences that stay, and new lengths int32 [n])."""
+        [n, new_max_blocks], rows of -1 for sequences that stay, and new lengths int32 [n]).  All or
+        nothing: where the pool lacks the fresh blocks of all, go by fewer sequences at a time."""
         new_max_blocks = new_max_blocks or -(-int(budget) // self.block_size)
         ids = torch.tensor(list(sids), dtype=torch.int64)
         t = torch.empty((len(sids), new_max_blocks), dtype=torch.int32)
