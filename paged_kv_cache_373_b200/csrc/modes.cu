@@ -10,9 +10,9 @@
 // bytes once); 3 sequences of up to 301 tokens 6.0 us; 16 FP8 sequences with a window
 // of 4096 and 64 kept tokens 35 us, 3900 GB/s, of which 25 us are the tile loop (5400
 // GB/s) and the rest its start and the merge.  With weights: 64 sequences of 64 to
-// 8192 tokens 86 us, 5220 GB/s: the decode pass 74, the merge 4, the weights pass 8 (its
+// 8192 tokens 87 us, 5150 GB/s: the decode pass some 75, the merge 4, the weights pass 8 (its
 // scores, 4 bytes per q head and token, written once and read once, mostly in L2);
-// 5 sequences of up to 777 tokens 7.0 us.
+// 5 sequences of up to 777 tokens 7.4 us (f16: 0.2 of them for its second sum per row).
 #include <cfloat>
 #include <cmath>
 

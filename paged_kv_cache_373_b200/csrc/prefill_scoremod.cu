@@ -36,17 +36,20 @@
 // Measured (8192 rows of 16 / 8 heads of 128, bf16, scores capped; the last chunk of
 // 2048 rows of 32 / 8 heads at 6100 with a window of 1024 and a prefix of 200): 160 us,
 // 660 TFLOP/s of the algorithm's operations (P's lo part adds half as many again), and
-// 66 to 73 us; one prompt of 8192 rows of 32 / 8 heads, capped, 800 TFLOP/s.  The plain prefill kernel's
+// 66 to 73 us, replayed from a graph over the same inputs (called on changing ones 184 to 188
+// and 74); one prompt of 8192 rows of 32 / 8 heads, capped, 800 TFLOP/s.  The plain prefill kernel's
 // structure with these scores (two threads per row, one S buffer) took 294 and 123 us.
-// What it took: the issuing warp run uniformly with an elected lane (one lane's branch
+// What it took: 64-token tiles with two S buffers per unit and a cheaper cap, 284 -> 224
+// and 159 -> 99; the issuing warp run uniformly with an elected lane (one lane's branch
 // made every descriptor a vector register that the instruction had to fetch: 75 cycles a
-// product) 284 -> 224 and 159 -> 99; its waits as shared-memory counters -> 181 and
-// 70; the cap, the maxima and the exponentials in one run without a branch -> 165 and
-// 66; the pairs in the order of their lengths -> 160.  Bound now: the softmax warps, two per scheduler, whose instructions wait for each
-// other's results (the schedulers issue in 47 % of the cycles, the tensor core is busy
-// in 51 %, no pipe above 40 %).  Tried without gain: two threads per row (206 us: more
-// warps, but 40 % more instructions), P beside S with S released early (190 us),
-// 128-token tiles (284 us).
+// product), 3750 -> 2700 cycles per pair of tiles, and its waits as shared-memory
+// counters -> 181 and 70; the cap, the maxima and the exponentials in one run without a
+// branch -> 165 and 66; the pairs in the order of their lengths -> 160.  Bound now: the
+// softmax warps, two per scheduler, whose instructions wait for each other's results
+// (the schedulers issue in 47 % of the cycles, the tensor core is busy in 51 %, no pipe
+// above 40 %).  Tried without gain: two threads per row (206 us: more warps, but 40 %
+// more instructions), P beside S with S released early (190 us).  The 284 us are those of
+// 128-token tiles in the kernel's first form; in the present one they are not measured.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -386,6 +389,9 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
                     const float a = ex2(x.x), b = ex2(x.y);
                     const F2 ab = f2(a, b);
                     sum[e & 1] = f2_add(sum[e & 1], ab);
+                    // P in two bf16 parts, 16 bits; f16 keeps 11 in one, which next to the
+                    // output's own 11 raises its error by 15 % (0.00020 -> 0.00023 of its size)
+                    // and a second part would cost half as many products again
                     h[e] = pack2<kBf16>(a, b);
                     if constexpr (kBf16) {
                         const float2 hf = unpack2<true>(h[e]);

@@ -6,10 +6,12 @@
 
 namespace pkv {
 
-// tanh y, |relative error| < 2^-22: below 1/2 an odd polynomial (a minimax fit
-// of (tanh y) / y - 1 in y^2, off by 1.5e-8 at most), above it
-// 1 - 2 / (1 + e^2|y|) with the hardware's 2^x and reciprocal, whose sum is at
-// least 0.46 there and loses no digits to the subtraction.  y = +-inf gives +-1.
+// tanh y, |relative error| below 2.1 * 2^-22: below 1/2 an odd polynomial (a minimax
+// fit of (tanh y) / y - 1 in y^2, off by 1.6e-8 at most; with its roundings 0.4 *
+// 2^-22), above it 1 - 2 / (1 + e^2|y|) with the hardware's 2^x (documented to 2^-22)
+// and reciprocal (one unit in the last place).  That is worst at 1/2, where e^2|y|'s
+// error counts 0.39, the reciprocal's 2^-24 and the roundings of 1 + e and of the
+// difference 2^-25 in all, over a result of 0.46.  y = +-inf gives +-1.
 __device__ __forceinline__ float tanh_poly(float y) {
     const float z = y * y;
     float q = fmaf(z, 0.01724149100482464f, -0.05304549261927605f);
