@@ -448,8 +448,9 @@ pkv_status pkv_paged_attention_decode_cascade(void* out, const void* query, pkv_
  * Supported: f16 or bf16 caches with q and out of the same dtype,
  * head_dim in {64, 128}, block_size in {16, 32}, g in {1, 2, 4, 8, 16}
  * (otherwise PKV_EUNSUPPORTED).  A seq_len shorter than its chunk or longer
- * than its table row, or a decreasing query_start, sets PKV_DEVERR_SEQ_LEN
- * (those rows are not written); an out-of-range block id is read as block 0
+ * than its table row, or a query_start that decreases or leaves [0, num_query_tokens],
+ * sets PKV_DEVERR_SEQ_LEN (that sequence's rows are not written; of sequences whose chunks
+ * overlap some may be left out as well); an out-of-range block id is read as block 0
  * (the affected rows are unspecified) and sets PKV_DEVERR_BLOCK_ID.
  * num_query_tokens and num_blocks * block_size must stay below 2^31 (32-bit
  * copy coordinates; otherwise PKV_EUNSUPPORTED).  No workspace.  The

@@ -145,7 +145,7 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
             const int si = s0 + lane;
             int nrt = 0;
             if (si < p.num_seqs) {
-                const int C = __ldg(p.qstart + si + 1) - __ldg(p.qstart + si);
+                const int C = chunk_rows(p, si);
                 if (C < 0 && blockIdx.x == 0 && warp == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
                 nrt = C > 0 ? (int)(((int64_t)C * p.g + kPfRows - 1) / kPfRows) : 0;
             }
@@ -169,8 +169,7 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
         }
     }
     if (s < 0) return;  // past the last pair
-    const int q0 = __ldg(p.qstart + s);
-    const int C = __ldg(p.qstart + s + 1) - q0;
+    const int q0 = __ldg(p.qstart + s), C = chunk_rows(p, s);
     const int L = __ldg(p.seq_lens + s);
     if (L < C || L > p.mbps * p.bs) {
         if (tid == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
@@ -640,6 +639,7 @@ pkv_status prefill_prepare(PrefillParams* pp, int64_t* grid_out, void* out, cons
     p.qstart = query_start;
     p.err = err;
     p.num_blocks = num_blocks;
+    p.num_tokens = num_query_tokens;
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;

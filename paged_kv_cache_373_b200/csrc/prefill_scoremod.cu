@@ -165,14 +165,13 @@ __device__ __forceinline__ bool soft_sync_or(bool flag) {
 
 // Warp-collective, 2 to 32 sequences, one per lane: the u-th longest unit pair of all,
 // as (sequence, pair, the sequence's units); sequence -1 past the last.
-__device__ __forceinline__ int3 pair_by_length(const int32_t* qstart, const int32_t* seq_lens, int* err, int num_seqs,
-                                            int g, int units, int64_t u) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ int3 pair_by_length(const PrefillParams& p, int units, int64_t u) {
+    const int lane = threadIdx.x & 31, g = p.g;
     int C = 0, L = 0;
-    if (lane < num_seqs) {
-        C = __ldg(qstart + lane + 1) - __ldg(qstart + lane);
-        L = __ldg(seq_lens + lane);
-        if (C < 0 && blockIdx.x == 0 && threadIdx.x < 32) raise_error(err, PKV_DEVERR_SEQ_LEN);
+    if (lane < p.num_seqs) {
+        C = chunk_rows(p, lane);
+        L = __ldg(p.seq_lens + lane);
+        if (C < 0 && blockIdx.x == 0 && threadIdx.x < 32) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
     }
     const int nrt = C > 0 ? (int)(((int64_t)C * g + kRows - 1) / kRows) : 0;
     const int npr = (nrt + units - 1) / units;
@@ -228,7 +227,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
     const int64_t u = blockIdx.x / p.num_kv_heads;
     int s = -1, jp = 0, nrt_s = 0;
     if (p.num_seqs > 1 && p.num_seqs <= 32) {
-        const int3 at = pair_by_length(p.qstart, p.seq_lens, p.err, p.num_seqs, p.g, md.units, u);
+        const int3 at = pair_by_length(p, md.units, u);
         s = at.x;
         jp = at.y;
         nrt_s = at.z;
@@ -238,7 +237,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
             const int si = s0 + lane;
             int nrt = 0;
             if (si < p.num_seqs) {
-                const int C = __ldg(p.qstart + si + 1) - __ldg(p.qstart + si);
+                const int C = chunk_rows(p, si);
                 if (C < 0 && blockIdx.x == 0 && warp == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
                 nrt = C > 0 ? (int)(((int64_t)C * p.g + kRows - 1) / kRows) : 0;
             }
@@ -262,8 +261,7 @@ pkv_prefill_scoremod_kernel(const PrefillParams p, const __grid_constant__ CUten
         }
     }
     if (s < 0) return;  // past the last pair
-    const int q0 = __ldg(p.qstart + s);
-    const int C = __ldg(p.qstart + s + 1) - q0;
+    const int q0 = __ldg(p.qstart + s), C = chunk_rows(p, s);
     const int L = __ldg(p.seq_lens + s);
     if (L < C || L > p.mbps * p.bs) {
         if (tid == 0) raise_error(p.err, PKV_DEVERR_SEQ_LEN);
