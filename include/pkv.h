@@ -144,15 +144,15 @@ pkv_status pkv_reshape_and_cache(const void* key, const void* value, pkv_dtype s
  * head_dim contiguous elements; *_stride elements apart from token to token (at
  * least the row, a multiple of 16 bytes), so that all three may be column ranges
  * of one projection output.  query_out: [num_tokens, num_heads, head_dim]
- * contiguous; may be query itself when query is contiguous, else they must not
- * overlap.  positions: DEVICE int64 [num_tokens]; cos_sin: DEVICE fp32
- * [max_position, rotary_dim], both ignored when rotary_dim = 0 (no rotation).
+ * contiguous; may be query itself when query is contiguous, else it must not
+ * overlap the rows of query, key or value (PKV_EINVAL).  positions: DEVICE int64
+ * [num_tokens]; cos_sin: DEVICE fp32 [max_position, rotary_dim], both ignored when
+ * rotary_dim = 0 (no rotation).
  * slot_mapping entries >= 0 must be distinct.
  * dtype f32, f16 or bf16; cache_dtype the same, or FP8_E4M3 with k_scale and
  * v_scale; head_dim in {64, 128} (the attention calls read FP8 caches with 128 only);
- * rotary_dim a multiple of 16 up to head_dim
- * (PKV_EUNSUPPORTED otherwise).  All buffers but the scales, slots and positions
- * 16-byte aligned.
+ * rotary_dim a multiple of 16 up to head_dim (PKV_EUNSUPPORTED otherwise).  All
+ * buffers but the scales, slots and positions 16-byte aligned.
  */
 pkv_status pkv_qk_norm_rope_and_cache(void* query_out, const void* query, int64_t query_stride,
                                       const void* key, int64_t key_stride, const void* value,
@@ -309,7 +309,7 @@ pkv_status pkv_paged_attention_decode_scoremod(
  *   weights_out[s, kv, L-1] = w[L-1]    (the step's own token: its first weight)
  * and entries t >= L are left as they were.  weights_in, weights_out: DEVICE
  * fp32 [num_seqs, num_kv_heads, weight_len]; weights_in may be NULL (zeros) or
- * weights_out itself, else they must not overlap.  A sequence longer than
+ * weights_out itself, else they must not overlap (PKV_EINVAL).  A sequence longer than
  * weight_len sets PKV_DEVERR_SEQ_LEN (its first weight_len entries are written).
  * The weights are fp32 sums of fp32 probabilities in a fixed order (no atomics);
  * out is as pkv_paged_attention_decode gives it, from the same sums and roundings (its

@@ -443,17 +443,6 @@ evict_gather_kernel(const EvictParams p, int nblk, int parts, int lg_bs) {
     }
 }
 
-// A buffer of the call; bytes as a double, which no product of its sizes overflows.
-struct Span {
-    const char* name;
-    const void* at;
-    double bytes;
-};
-bool overlap(const Span& a, const Span& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-    return x <= y ? (double)(y - x) < a.bytes : (double)(x - y) < b.bytes;
-}
-
 }  // namespace
 }  // namespace pkv
 

@@ -143,6 +143,10 @@ extern "C" pkv_status pkv_paged_attention_decode_weights(
     size_t workspace_bytes, int num_ctas, pkv_stream_t stream) {
     if (weight_len <= 0) return fail(PKV_EINVAL, "weight_len must be positive");
     if (num_seqs > 0 && !weights_out) return fail(PKV_EINVAL, "null pointer");
+    const double weight_bytes = 4.0 * num_seqs * num_kv_heads * weight_len;
+    if (weights_in && weights_in != weights_out &&
+        overlap({"weights_in", weights_in, weight_bytes}, {"weights_out", weights_out, weight_bytes}))
+        return fail(PKV_EINVAL, "weights_in overlaps weights_out");
     DecodeParams p;
     DecodeLauncher plain;
     int grid = 0;

@@ -90,6 +90,17 @@ pkv_status launch_scores_fp8(const DecodeLaunchArgs&, const WeightsArg&, bool q_
 // The weights pass by itself, a programmatic dependent of the merge pass (modes.cu).
 pkv_status launch_weights_pass(const DecodeParams& p, const WeightsArg& a, int grid, cudaStream_t st);
 
+// A buffer of a call; bytes as a double, which no product of its sizes overflows.
+struct Span {
+    const char* name;
+    const void* at;
+    double bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x <= y ? (double)(y - x) < a.bytes : (double)(x - y) < b.bytes;
+}
+
 // The cap of modified scores in the log2 domain (cap2 = 0: none); PKV_EINVAL
 // for a cap that is negative, not finite or too small for fp32 arithmetic.
 pkv_status score_cap(float softcap, float* cap2, float* inv_cap2);

@@ -257,6 +257,15 @@ cudaError_t launch_rope_t(RopeParams& p, bool fp8, bool inter, cudaStream_t st) 
     return inter ? launch_rope<T, D, false, true>(p, st) : launch_rope<T, D, false, false>(p, st);
 }
 
+// Whether n rows of `row` bytes, `stride` apart, meet the n contiguous rows of `out_row`
+// bytes at `out`.
+bool rows_overlap(const void* rows, int64_t stride, int64_t row, const void* out, int64_t out_row, int64_t n) {
+    const double d = (double)(intptr_t)((uintptr_t)out - (uintptr_t)rows);  // out, seen from the first row
+    // the first row that ends behind out's start
+    const double i = d < (double)row ? 0.0 : std::floor((d - (double)row) / (double)stride) + 1.0;
+    return i < (double)n && i * (double)stride < d + (double)out_row * (double)n;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -300,6 +309,12 @@ extern "C" pkv_status pkv_qk_norm_rope_and_cache(
         return fail(PKV_EINVAL, "buffers must be 16-byte aligned");
     if (query == query_out && query_stride != want[0])
         return fail(PKV_EINVAL, "query_out in place of a query with another token stride");
+    // query_out apart from the rows that are read (or exactly query, row by row)
+    const void* rows[3] = {query, key, value};
+    const char* names[3] = {"query", "key", "value"};
+    for (int i = query == query_out ? 1 : 0; i < 3; ++i)
+        if (rows_overlap(rows[i], have[i] * eb, want[i] * eb, query_out, want[0] * eb, num_tokens))
+            return fail(PKV_EINVAL, "query_out overlaps %s", names[i]);
     int* err = device_error_word();
     if (!err) return fail(PKV_ECUDA, "device error word unavailable");
     RopeParams p{};
