@@ -141,7 +141,8 @@ pkv_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm
     int s = -1, jp = 0, nrt_s = 0;
     {
         int64_t base = 0;
-        for (int s0 = 0; s0 < p.num_seqs && s < 0; s0 += 32) {
+        // (block 0 goes through all of them, for its check)
+        for (int s0 = 0; s0 < p.num_seqs && (s < 0 || blockIdx.x == 0); s0 += 32) {
             const int si = s0 + lane;
             int nrt = 0;
             if (si < p.num_seqs) {

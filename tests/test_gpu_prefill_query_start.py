@@ -18,7 +18,7 @@ CASES = [([0, 450, T], -1), ([-30, 100, T], 1), ([0, 100, 400], 0), ([0, 300, 30
 
 @pytest.mark.parametrize("starts,right", CASES, ids=lambda x: "_".join(map(str, x)) if isinstance(x, list) else "")
 @pytest.mark.parametrize("call", ["plain", "scoremod", "bias"])
-@pytest.mark.parametrize("empty", [0, 40])  # more sequences without rows: the search by length ends at 32
+@pytest.mark.parametrize("empty", [0, 40])  # sequences without rows between: the search by length ends at 32
 @pytest.mark.parametrize("g", [1, 16])      # few units, and more than SMs
 def test_flagged_and_nothing_outside_written(starts, right, call, empty, g):
     d = cuda(build([L, L], HKV, D, BS, torch.float16, 95))
@@ -27,10 +27,10 @@ def test_flagged_and_nothing_outside_written(starts, right, call, empty, g):
     room = torch.full((1024, Hq, D), 9.0, dtype=torch.float16, device="cuda")
     out = room[400:400 + T]
     tables = torch.full((S, d["tables"].shape[1]), -1, dtype=torch.int32, device="cuda")
-    tables[:2] = d["tables"]
+    tables[[0, S - 1]] = d["tables"]
     lens = torch.zeros(S, dtype=torch.int32, device="cuda")
-    lens[:2] = L
-    qs = torch.tensor(starts + [starts[-1]] * empty, dtype=torch.int32, device="cuda")
+    lens[[0, S - 1]] = L
+    qs = torch.tensor(starts[:2] + [starts[1]] * empty + starts[2:], dtype=torch.int32, device="cuda")
     slopes = torch.linspace(0.02, 0.7, Hq).cuda()
     if call == "plain":
         pkv.paged_prefill(out, q, d["kc"], d["vc"], tables, lens, qs, SCALE)
